@@ -68,6 +68,13 @@ SIGNATURES = {
                                   _P]),
     "mla_decode_absorbed_fp8": (_S, [_D, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t,
                                      _P]),
+    "mla_append_paged": (_S, [_D, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                              _P, ctypes.c_int64, _P, ctypes.c_int32, _P]),
+    "mla_append_paged_q8": (_S, [_D, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int32,
+                                 ctypes.c_int32, _P, _P, ctypes.c_int64, _P, ctypes.c_int32, _P]),
+    "mla_decode_q8_workspace_size": (ctypes.c_size_t, [_D, ctypes.c_int32, ctypes.c_int32]),
+    "mla_decode_absorbed_paged_q8": (_S, [_D, _P, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int32, _P,
+                                          ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
     "mla_rope_apply": (_S, [_P, _P, ctypes.c_int64, _P, _P]),
     "mla_set_wait_limit": (_S, [ctypes.c_uint32]),
     "mla_test_starve_projection": (_S, [ctypes.c_int32]),
@@ -269,6 +276,107 @@ def mla_decode_absorbed_fp8(dims, weights: MLAWeights, cache_fp8, offsets, out, 
     _check(_lib.mla_decode_absorbed_fp8(ctypes.byref(dims), weights.handle, _ptr(q_nope), _ptr(q_rope),
                                         _ptr(cache_fp8), cache_fp8.shape[0], _ptr(offsets), B, _ptr(out), _ptr(ws),
                                         ws.numel(), _stream(stream)), "mla_decode_absorbed_fp8")
+
+
+# The paged-cache calls below check what the C ABI cannot see behind a pointer (types, shapes,
+# strides, devices) and run on the tensors' own device, whichever is current.
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name: str, dtype, shape, device) -> ctypes.c_void_p:
+    """Device pointer of a contiguous tensor of this type, shape (None: any extent) and device."""
+    _need(t.dtype == dtype, f"{name}: {t.dtype}, not {dtype}")
+    _need(t.dim() == len(shape) and all(w is None or g == w for g, w in zip(t.shape, shape)),
+          f"{name}: shape {tuple(t.shape)}, not {tuple('any' if w is None else w for w in shape)}")
+    _need(t.is_cuda and t.device == device, f"{name}: on {t.device}, not {device}")
+    _need(t.is_contiguous(), f"{name}: not contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t, name: str, dtype, n: int, width: int, device):
+    """(pointer, row stride in elements) of an [n, width] tensor with contiguous rows."""
+    _need(t.dtype == dtype, f"{name}: {t.dtype}, not {dtype}")
+    _need(t.dim() == 2 and t.shape[0] == n and t.shape[1] == width, f"{name}: shape {tuple(t.shape)}, not {(n, width)}")
+    _need(t.is_cuda and t.device == device, f"{name}: on {t.device}, not {device}")
+    _need(t.stride(1) == 1 or n == 0, f"{name}: columns are not contiguous")
+    ld = t.stride(0) if n > 1 else max(width, t.stride(0))
+    _need(ld >= width or n == 0, f"{name}: rows overlap (stride {ld}, width {width})")
+    return ctypes.c_void_p(t.data_ptr()), max(ld, width)
+
+
+def _storage(dims):
+    return torch.bfloat16 if dims.dtype == MLA_BF16 else torch.float32
+
+
+def _append_paged_args(dims, c, k_r, new_offsets, seq_lens, block_table, pos, device):
+    n, B = c.shape[0], seq_lens.numel()
+    st = _storage(dims)
+    cp, ld_c = _rows(c, "c", st, n, dims.d_c, device)
+    kp, ld_k = _rows(k_r, "k_r", st, n, dims.d_hR, device)
+    i32 = torch.int32
+    return (cp, ld_c, kp, ld_k, _tensor(new_offsets, "new_offsets", i32, (B + 1,), device),
+            _tensor(seq_lens, "seq_lens", i32, (B,), device),
+            None if pos is None else _tensor(pos, "pos", i32, (n,), device), B, n,
+            _tensor(block_table, "block_table", i32, (B, None), device), block_table.shape[1])
+
+
+def mla_append_paged(dims, c, k_r, new_offsets, seq_lens, cache_pages, block_table, pos=None, stream=None) -> None:
+    """Append latents c [n, d_c] and unrotated keys k_r [n, d_hR] (rows may be strided) to a
+    paged cache [num_pages, 64, d_c + d_hR], rotating the keys: sequence b's new tokens are rows
+    new_offsets[b] .. new_offsets[b+1] - 1 (int32 [B+1]) and the last of its seq_lens[b] tokens
+    (int32 [B], after the append); block_table int32 [B, max_blocks]; pos int32 [n] or the
+    tokens' places in their sequences."""
+    dev = cache_pages.device
+    with torch.cuda.device(dev):
+        cp, ld_c, kp, ld_k, no, sl, pp, B, n, bt, mb = _append_paged_args(dims, c, k_r, new_offsets, seq_lens,
+                                                                          block_table, pos, dev)
+        pages = _tensor(cache_pages, "cache_pages", _storage(dims), (None, 64, dims.d_c + dims.d_hR), dev)
+        _check(_lib.mla_append_paged(ctypes.byref(dims), cp, ld_c, kp, ld_k, no, sl, pp, B, n, pages,
+                                     cache_pages.shape[0], bt, mb, _stream(stream)), "mla_append_paged")
+
+
+def mla_append_paged_q8(dims, c, k_r, new_offsets, seq_lens, codes, scales, block_table, pos=None,
+                        stream=None) -> None:
+    """mla_append_paged into an 8-bit cache: codes uint8 [num_pages, 64, 576] (FP8 E4M3), scales
+    float32 [num_pages], one power of two per page (value = code * scale)."""
+    dev = codes.device
+    with torch.cuda.device(dev):
+        cp, ld_c, kp, ld_k, no, sl, pp, B, n, bt, mb = _append_paged_args(dims, c, k_r, new_offsets, seq_lens,
+                                                                          block_table, pos, dev)
+        cd = _tensor(codes, "codes", torch.uint8, (None, 64, dims.d_c + dims.d_hR), dev)
+        sc = _tensor(scales, "scales", torch.float32, (codes.shape[0],), dev)
+        _check(_lib.mla_append_paged_q8(ctypes.byref(dims), cp, ld_c, kp, ld_k, no, sl, pp, B, n, cd, sc,
+                                        codes.shape[0], bt, mb, _stream(stream)), "mla_append_paged_q8")
+
+
+def mla_decode_q8_workspace_size(dims, B: int, q_len: int = 1) -> int:
+    return int(_lib.mla_decode_q8_workspace_size(ctypes.byref(dims), B, q_len))
+
+
+def mla_decode_absorbed_paged_q8(dims, weights: MLAWeights, codes, scales, block_table, seq_lens, out, ws, q_nope,
+                                 q_rope, stream=None) -> None:
+    """Absorbed decode over the 8-bit paged cache: q_nope [B, q_len, H, 128], q_rope
+    [B, q_len, H, 64], out [B, q_len, H, 128] (bf16); the q_len new tokens are the last q_len
+    of each sequence's seq_lens[b] tokens, already appended."""
+    dev = codes.device
+    _need(q_nope.dim() == 4, f"q_nope: shape {tuple(q_nope.shape)}, not [B, q_len, H, qk_nope]")
+    B, Q = q_nope.shape[:2]
+    with torch.cuda.device(dev):
+        bf, i32 = torch.bfloat16, torch.int32
+        qn = _tensor(q_nope, "q_nope", bf, (B, Q, dims.H, dims.qk_nope), dev)
+        qr = _tensor(q_rope, "q_rope", bf, (B, Q, dims.H, dims.d_hR), dev)
+        op = _tensor(out, "out", bf, (B, Q, dims.H, dims.v_head), dev)
+        cd = _tensor(codes, "codes", torch.uint8, (None, 64, dims.d_c + dims.d_hR), dev)
+        sc = _tensor(scales, "scales", torch.float32, (codes.shape[0],), dev)
+        bt = _tensor(block_table, "block_table", i32, (B, None), dev)
+        sl = _tensor(seq_lens, "seq_lens", i32, (B,), dev)
+        wp = _tensor(ws, "ws", torch.uint8, (None,), dev)
+        _check(_lib.mla_decode_absorbed_paged_q8(ctypes.byref(dims), weights.handle, qn, qr, cd, sc, codes.shape[0],
+                                                 bt, block_table.shape[1], sl, B, Q, op, wp, ws.numel(),
+                                                 _stream(stream)), "mla_decode_absorbed_paged_q8")
 
 
 def mla_prefill_causal(dims, weights: MLAWeights, h, W_DKV, W_KR, cache, out, ws, stream=None) -> None:

@@ -6,10 +6,13 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "decode_q8.cuh"
 #include "decode_tc.cuh"
 #include "fp8.cuh"
 #include "gemm_tc.cuh"
 #include "multi.cuh"
+#include "paged.cuh"
+#include "paged_plan.h"
 #include "prefill_tc.cuh"
 #include "mla.h"
 
@@ -791,6 +794,147 @@ extern "C" mla_status mla_decode_absorbed_fp8(const mla_dims* d, mla_weights w, 
         (const bf16*)w->ukt_tiled, (const bf16*)w->uv_tiled, cache_fp8, true, cache_rows, offsets, nullptr, nullptr, 0,
         B, 1, true, scale_of(d), (bf16*)out, ws.tc, num_sms(), err.code, err.detail, (cudaStream_t)stream);
     return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_absorbed_fp8");
+}
+
+// ---------------------------------------------------- paged append, 8-bit pages
+
+static bool aligned_to(const void* p, size_t k) { return ((uintptr_t)p & (k - 1)) == 0; }
+
+// The row shape of the 8-bit pages and their decode: the V2/V3 latent and key widths in bf16,
+// for any share of the 128 heads.
+static bool q8_rows_ok(const mla_dims* d) {
+    return d->dtype == MLA_BF16 && d->d_c == mla::tc::kDc && d->d_hR == mla::tc::kDr;
+}
+static bool q8_decode_ok(const mla_dims* d) {
+    return q8_rows_ok(d) && d->H <= mla::tc::kH && d->qk_nope == 128 && d->v_head == 128;
+}
+
+// The argument checks both paged appends share; n = 0 is settled by the caller.
+static mla_status append_paged_args(const mla_dims* d, const mla::AppendPaged& a, const void* cache) {
+    const size_t es = esize(d);
+    if (a.B <= 0 || !a.c || !a.k_r || !a.new_offsets || !a.seq_lens || !a.block_table || !cache || a.num_pages <= 0 ||
+        a.max_blocks <= 0 || a.ld_c < d->d_c || a.ld_kr < d->d_hR)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned_to(a.c, es) || !aligned_to(a.k_r, es) || !aligned_to(cache, es) || !aligned_to(a.new_offsets, 4) ||
+        !aligned_to(a.seq_lens, 4) || !aligned_to(a.block_table, 4) || !aligned_to(a.pos, 4))
+        return MLA_ERR_INVALID_ARG;
+    if (d->d_hR / 2 > mla::kMaxRopePairs || mla::append_items(a.n, a.B) > 0x7FFFFFFFLL) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+extern "C" mla_status mla_append_paged(const mla_dims* d, const void* c, int64_t ld_c, const void* k_r, int64_t ld_kr,
+                                       const int32_t* new_offsets, const int32_t* seq_lens, const int32_t* pos,
+                                       int32_t B, int32_t n, void* cache, int64_t num_pages,
+                                       const int32_t* block_table, int32_t max_blocks, mla_stream_t stream) {
+    mla_status st = dims_supported(d);
+    if (st != MLA_OK) return st;
+    if (n < 0 || B < 0) return MLA_ERR_INVALID_ARG;
+    if (n == 0) return MLA_OK;
+    const mla::AppendPaged a{c, k_r, ld_c, ld_kr, new_offsets, seq_lens, pos, block_table, B, n, max_blocks, num_pages,
+                             d->d_c, d->d_hR};
+    if ((st = append_paged_args(d, a, cache)) != MLA_OK) return st;
+    DevErr err;
+    if ((st = dev_err(&err)) != MLA_OK) return st;
+    mla::ProfScope ps((cudaStream_t)stream, "append_paged");
+    cudaError_t e = d->dtype == MLA_BF16
+                        ? mla::append_paged<bf16>(a, theta_of(d), (bf16*)cache, err, (cudaStream_t)stream)
+                        : mla::append_paged<float>(a, theta_of(d), (float*)cache, err, (cudaStream_t)stream);
+    return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_append_paged");
+}
+
+extern "C" mla_status mla_append_paged_q8(const mla_dims* d, const void* c, int64_t ld_c, const void* k_r,
+                                          int64_t ld_kr, const int32_t* new_offsets, const int32_t* seq_lens,
+                                          const int32_t* pos, int32_t B, int32_t n, void* codes, float* scales,
+                                          int64_t num_pages, const int32_t* block_table, int32_t max_blocks,
+                                          mla_stream_t stream) {
+    mla_status st = dims_supported(d);
+    if (st != MLA_OK) return st;
+    if (!q8_rows_ok(d)) return MLA_ERR_UNSUPPORTED;
+    if (n < 0 || B < 0) return MLA_ERR_INVALID_ARG;
+    if (n == 0) return MLA_OK;
+    const mla::AppendPaged a{c, k_r, ld_c, ld_kr, new_offsets, seq_lens, pos, block_table, B, n, max_blocks, num_pages,
+                             d->d_c, d->d_hR};
+    if ((st = append_paged_args(d, a, codes)) != MLA_OK) return st;
+    if (!scales || !aligned_to(scales, 4) || !aligned16(codes)) return MLA_ERR_INVALID_ARG;
+    DevErr err;
+    if ((st = dev_err(&err)) != MLA_OK) return st;
+    mla::ProfScope ps((cudaStream_t)stream, "append_paged_q8");
+    cudaError_t e = mla::append_paged_q8(a, theta_of(d), (uint8_t*)codes, scales, err, (cudaStream_t)stream);
+    return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_append_paged_q8");
+}
+
+struct Q8Ws {
+    float* q_lat;     // [B q_len, H, 512]
+    float* part_o;    // [ns, B q_len, H, 512]
+    float* part_ml;   // [ns, B q_len, H, 2]
+    float* o_lat;     // [B q_len, H, 512]
+    int ns;
+    size_t bytes;
+};
+
+static Q8Ws carve_q8(const mla_dims* d, int B, int q_len, void* base) {
+    Carve c(base);
+    Q8Ws w{};
+    const int NV = B * q_len;
+    const size_t rows = (size_t)NV * d->H;
+    w.ns = simt_splits(NV, d->H);
+    w.q_lat = (float*)c.take(rows * d->d_c * 4);
+    w.part_o = (float*)c.take(w.ns * rows * d->d_c * 4);
+    w.part_ml = (float*)c.take(w.ns * rows * 2 * 4);
+    w.o_lat = (float*)c.take(rows * d->d_c * 4);
+    w.bytes = c.used;
+    return w;
+}
+
+static bool q8_sizes_ok(int32_t B, int32_t q_len) {
+    return B >= 0 && q_len >= 1 && (long long)B * q_len <= 65535;
+}
+
+extern "C" size_t mla_decode_q8_workspace_size(const mla_dims* d, int32_t B, int32_t q_len) {
+    if (dims_supported(d) != MLA_OK || !q8_decode_ok(d) || !q8_sizes_ok(B, q_len)) return 0;
+    return carve_q8(d, B, q_len, nullptr).bytes;
+}
+
+extern "C" mla_status mla_decode_absorbed_paged_q8(const mla_dims* d, mla_weights w, const void* q_nope,
+                                                   const void* q_rope, const void* codes, const float* scales,
+                                                   int64_t num_pages, const int32_t* block_table, int32_t max_blocks,
+                                                   const int32_t* seq_lens, int32_t B, int32_t q_len, void* out,
+                                                   void* workspace, size_t ws_bytes, mla_stream_t stream) {
+    mla_status st = dims_supported(d);
+    if (st != MLA_OK) return st;
+    if (!w || B < 0 || q_len < 1) return MLA_ERR_INVALID_ARG;
+    if (memcmp(&w->dims, d, sizeof(mla_dims)) != 0) return MLA_ERR_INVALID_ARG;
+    if (!q8_decode_ok(d) || w->W_O) return MLA_ERR_UNSUPPORTED;
+    if (B == 0) return MLA_OK;
+    if (!q_nope || !q_rope || !codes || !scales || !block_table || !seq_lens || !out || max_blocks <= 0 ||
+        num_pages <= 0)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(out) || !aligned16(codes) || !aligned_to(scales, 4) ||
+        !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4))
+        return MLA_ERR_INVALID_ARG;
+    if (!q8_sizes_ok(B, q_len) || num_pages * (long long)mla::kPageRows > 0x7FFFFFFFLL) return MLA_ERR_UNSUPPORTED;
+    int device = -1;
+    MLA_CUDA(cudaGetDevice(&device));
+    if (device != w->device) return MLA_ERR_INVALID_ARG;
+    Q8Ws ws = carve_q8(d, B, q_len, workspace);
+    if (!workspace || ws_bytes < ws.bytes || ((uintptr_t)workspace & 255)) return MLA_ERR_WORKSPACE;
+    DevErr err;
+    if ((st = dev_err(&err)) != MLA_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    const mla::q8::Problem p{d->H, B, q_len, (const uint8_t*)codes, scales, num_pages, block_table, seq_lens,
+                             max_blocks, scale_of(d)};
+    const int NV = B * q_len;
+    const long long H = d->H, dc = d->d_c, qk = d->qk_nope, vh = d->v_head;
+    cudaError_t e = mla::launch_gemm_nt<bf16, bf16, float>(d->H, NV, d->d_c, d->qk_nope, (const bf16*)q_nope, qk,
+                                                           H * qk, 1, (const bf16*)w->W_UKT, dc * qk, qk, 1, ws.q_lat,
+                                                           dc, H * dc, 1, s);
+    if (e == cudaSuccess)
+        e = mla::q8::decode_split(p, ws.q_lat, (const bf16*)q_rope, ws.ns, ws.part_o, ws.part_ml, err, s);
+    if (e == cudaSuccess) e = mla::launch_combine(ws.part_o, ws.part_ml, ws.ns, NV, d->H, d->d_c, ws.o_lat, s);
+    if (e == cudaSuccess)
+        e = mla::launch_gemm_nt<float, bf16, bf16>(d->H, NV, d->v_head, d->d_c, ws.o_lat, dc, H * dc, 1,
+                                                   (const bf16*)w->W_UV, vh * dc, dc, 1, (bf16*)out, vh, H * vh, 1, s);
+    return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_absorbed_paged_q8");
 }
 
 // ----------------------------------------------------------------------- prefill

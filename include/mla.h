@@ -313,6 +313,78 @@ mla_status mla_decode_absorbed_fp8(const mla_dims* dims, mla_weights w, const vo
                                    const int32_t* offsets, int32_t B, void* out, void* workspace,
                                    size_t ws_bytes, mla_stream_t stream);
 
+/* ------------------------------------------------- paged append, 8-bit paged cache */
+
+/* Appending GIVEN latents and rotary keys to a paged cache, with the rotation on the way.
+ * mla_append_cache computes the row from the hidden state; these calls take the latent and
+ * the unrotated key themselves, for models that do something to the latent between the
+ * down-projection and the cache (a norm, as DeepSeek-V2/V3 have) and for caches in pages
+ * ["DeepSeek MLA", the PagedAttention comparison].
+ *
+ * B sequences receive n tokens in all: sequence b's new tokens are rows new_offsets[b] ..
+ * new_offsets[b+1] - 1 of c and k_r (int32 [B+1], device, new_offsets[0] = 0,
+ * new_offsets[B] = n) and become the last of its seq_lens[b] tokens (int32 [B], device: the
+ * lengths AFTER the append, as the decode of the same step takes them).  Any number of new
+ * tokens per sequence, none included.  Token j of a sequence is row j % 64 of page
+ * block_table[b * max_blocks + j / 64] (int32 [B, max_blocks], device), and that row becomes
+ *     [c_i | RoPE(k_r,i, p)],   p = pos[i] (int32 [n], device), or j where pos is NULL.
+ *   c [n, d_c] with rows ld_c elements apart, k_r [n, d_hR] with rows ld_kr elements apart
+ *   (both may be column slices of one projection output); they must not overlap the cache.
+ * Only the rows of the new tokens are written.  A page that receives tokens belongs to one
+ * sequence (two sequences of one call that write the same page race).  Errors found on the
+ * device latch MLA_ERR_OUT_OF_RANGE: offsets that are negative, decreasing, or do not cover
+ * exactly 0 .. n (nothing is written), a sequence with fewer tokens than new ones or more
+ * than max_blocks pages (skipped), a page outside [0, num_pages) (its rows are skipped).
+ * n = 0 is a no-op. */
+
+/* Into pages of the storage type: cache [num_pages, 64, d_c + d_hR], as
+ * mla_decode_absorbed_paged and mla_decode_absorbed_paged_multi read it (fp32 or bf16; every
+ * width the library supports). */
+mla_status mla_append_paged(const mla_dims* dims, const void* c, int64_t ld_c, const void* k_r, int64_t ld_kr,
+                            const int32_t* new_offsets, const int32_t* seq_lens, const int32_t* pos, int32_t B,
+                            int32_t n, void* cache, int64_t num_pages, const int32_t* block_table,
+                            int32_t max_blocks, mla_stream_t stream);
+
+/* Into 8-bit pages: codes [num_pages, 64, 576] FP8 E4M3, and one fp32 scale per page (the
+ * cache has one latent head, which all query heads share): value = code * scales[page].
+ * 576 bytes per token, half of a bf16 row, latent and key alike.  The scale is the smallest power
+ * of two s with amax <= 448 s, amax over the finite new values of the page (1 if they are all
+ * zero; at least 2^-60).  On a page that holds earlier tokens it never shrinks, and when it
+ * grows their codes are re-expressed under it, exactly but for codes that become subnormal
+ * (those round to nearest even).  code = e4m3(value / s), nearest even; values past 448 s
+ * (infinities) saturate, NaN stays NaN.  scales of pages that start with this call need not
+ * hold anything.  bf16, d_c = 512, d_hR = 64 only, else MLA_ERR_UNSUPPORTED (H, qk_nope,
+ * v_head and d_model do not matter); codes 16-byte aligned. */
+mla_status mla_append_paged_q8(const mla_dims* dims, const void* c, int64_t ld_c, const void* k_r, int64_t ld_kr,
+                               const int32_t* new_offsets, const int32_t* seq_lens, const int32_t* pos, int32_t B,
+                               int32_t n, void* codes, float* scales, int64_t num_pages,
+                               const int32_t* block_table, int32_t max_blocks, mla_stream_t stream);
+
+/* Workspace bytes of mla_decode_absorbed_paged_q8 on the current device; 0 for shapes it does
+ * not support or sizes out of range (B < 0, q_len < 1, B * q_len > 65535). */
+size_t mla_decode_q8_workspace_size(const mla_dims* dims, int32_t B, int32_t q_len);
+
+/* Absorbed decode over the 8-bit paged cache, q_len >= 1 new tokens per sequence (their rows
+ * already appended): arguments, lengths and the causal rule as for
+ * mla_decode_absorbed_paged_multi, on the values code * scales[page].
+ *   q_nope [B, q_len, H, 128], q_rope [B, q_len, H, 64] (rotated), out [B, q_len, H, 128]:
+ *   device, bf16, contiguous, 16-byte aligned; codes 16-byte aligned.
+ * Any head count up to 128 (a head-parallel layer's share of the heads), bf16, d_c = 512,
+ * d_hR = 64, qk_nope = v_head = 128 and handles without W_O, else MLA_ERR_UNSUPPORTED.  The
+ * scales of the pages in use must be positive and finite (any such value, not only powers of
+ * two).  What the pages hold behind a sequence's last token does not matter, NaN codes
+ * included.  A token with no key gets zeros.  A sequence with a negative length or more than
+ * max_blocks pages latches MLA_ERR_OUT_OF_RANGE and decodes to zeros; a page outside
+ * [0, num_pages) latches the same error and its tokens are taken as zero rows.
+ * Results do not depend on the order of execution: equal calls give equal bits.
+ * Workspace: device, >= mla_decode_q8_workspace_size(dims, B, q_len) bytes, 256-byte aligned,
+ * contents on entry do not matter; calls that may overlap need one each. */
+mla_status mla_decode_absorbed_paged_q8(const mla_dims* dims, mla_weights w, const void* q_nope,
+                                        const void* q_rope, const void* codes, const float* scales,
+                                        int64_t num_pages, const int32_t* block_table, int32_t max_blocks,
+                                        const int32_t* seq_lens, int32_t B, int32_t q_len, void* out,
+                                        void* workspace, size_t ws_bytes, mla_stream_t stream);
+
 /* ---------------------------------------------------------------- causal prefill */
 
 /* Bytes of workspace mla_prefill_causal needs for B sequences of S tokens. */
