@@ -863,36 +863,13 @@ extern "C" mla_status mla_append_paged_q8(const mla_dims* d, const void* c, int6
     return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_append_paged_q8");
 }
 
-struct Q8Ws {
-    float* q_lat;     // [B q_len, H, 512]
-    float* part_o;    // [ns, B q_len, H, 512]
-    float* part_ml;   // [ns, B q_len, H, 2]
-    float* o_lat;     // [B q_len, H, 512]
-    int ns;
-    size_t bytes;
-};
-
-static Q8Ws carve_q8(const mla_dims* d, int B, int q_len, void* base) {
-    Carve c(base);
-    Q8Ws w{};
-    const int NV = B * q_len;
-    const size_t rows = (size_t)NV * d->H;
-    w.ns = simt_splits(NV, d->H);
-    w.q_lat = (float*)c.take(rows * d->d_c * 4);
-    w.part_o = (float*)c.take(w.ns * rows * d->d_c * 4);
-    w.part_ml = (float*)c.take(w.ns * rows * 2 * 4);
-    w.o_lat = (float*)c.take(rows * d->d_c * 4);
-    w.bytes = c.used;
-    return w;
-}
-
 static bool q8_sizes_ok(int32_t B, int32_t q_len) {
     return B >= 0 && q_len >= 1 && (long long)B * q_len <= 65535;
 }
 
 extern "C" size_t mla_decode_q8_workspace_size(const mla_dims* d, int32_t B, int32_t q_len) {
     if (dims_supported(d) != MLA_OK || !q8_decode_ok(d) || !q8_sizes_ok(B, q_len)) return 0;
-    return carve_q8(d, B, q_len, nullptr).bytes;
+    return mla::q8::carve(nullptr, mla::q8::make_shape(B, q_len, d->H, num_sms())).bytes;
 }
 
 extern "C" mla_status mla_decode_absorbed_paged_q8(const mla_dims* d, mla_weights w, const void* q_nope,
@@ -916,24 +893,15 @@ extern "C" mla_status mla_decode_absorbed_paged_q8(const mla_dims* d, mla_weight
     int device = -1;
     MLA_CUDA(cudaGetDevice(&device));
     if (device != w->device) return MLA_ERR_INVALID_ARG;
-    Q8Ws ws = carve_q8(d, B, q_len, workspace);
+    const mla::q8::Shape shape = mla::q8::make_shape(B, q_len, d->H, num_sms());
+    const mla::q8::Ws ws = mla::q8::carve((char*)workspace, shape);
     if (!workspace || ws_bytes < ws.bytes || ((uintptr_t)workspace & 255)) return MLA_ERR_WORKSPACE;
     DevErr err;
     if ((st = dev_err(&err)) != MLA_OK) return st;
-    cudaStream_t s = (cudaStream_t)stream;
-    const mla::q8::Problem p{d->H, B, q_len, (const uint8_t*)codes, scales, num_pages, block_table, seq_lens,
-                             max_blocks, scale_of(d)};
-    const int NV = B * q_len;
-    const long long H = d->H, dc = d->d_c, qk = d->qk_nope, vh = d->v_head;
-    cudaError_t e = mla::launch_gemm_nt<bf16, bf16, float>(d->H, NV, d->d_c, d->qk_nope, (const bf16*)q_nope, qk,
-                                                           H * qk, 1, (const bf16*)w->W_UKT, dc * qk, qk, 1, ws.q_lat,
-                                                           dc, H * dc, 1, s);
-    if (e == cudaSuccess)
-        e = mla::q8::decode_split(p, ws.q_lat, (const bf16*)q_rope, ws.ns, ws.part_o, ws.part_ml, err, s);
-    if (e == cudaSuccess) e = mla::launch_combine(ws.part_o, ws.part_ml, ws.ns, NV, d->H, d->d_c, ws.o_lat, s);
-    if (e == cudaSuccess)
-        e = mla::launch_gemm_nt<float, bf16, bf16>(d->H, NV, d->v_head, d->d_c, ws.o_lat, dc, H * dc, 1,
-                                                   (const bf16*)w->W_UV, vh * dc, dc, 1, (bf16*)out, vh, H * vh, 1, s);
+    const mla::q8::Problem p{(const bf16*)q_nope, (const bf16*)q_rope, (const bf16*)w->W_UKT, (const bf16*)w->W_UV,
+                             (const uint8_t*)codes, scales, num_pages, block_table, seq_lens, max_blocks, scale_of(d),
+                             (bf16*)out};
+    const cudaError_t e = mla::q8::decode(p, shape, ws, err, (cudaStream_t)stream);
     return e == cudaSuccess ? MLA_OK : cuda_fail(e, "mla_decode_absorbed_paged_q8");
 }
 
@@ -1079,6 +1047,7 @@ extern "C" mla_status mla_set_wait_limit(uint32_t polls) {
     MLA_CUDA(mla::tc::set_wait_limit_decode(p));
     MLA_CUDA(mla::tc::set_wait_limit_gemm(p));
     MLA_CUDA(mla::tc::set_wait_limit_prefill(p));
+    MLA_CUDA(mla::q8::set_wait_limit_decode_q8(p));
     return MLA_OK;
 }
 

@@ -1,116 +1,1224 @@
-// Absorbed attention over the 8-bit paged latent cache.
+// Absorbed attention over the 8-bit paged latent cache, on the tcgen05 tensor cores.
 //
-// For query token v = (b, t), head h, cached token j (value row = code row * scale of its page):
-//     s_j = scale ([q_lat | q_rope][v, h] . row_j),   o_lat[v, h] = sum_j softmax(s)_j row_j[0:512]
-// over the first seq_lens[b] - q_len + t + 1 tokens of sequence b.
+// For query row r = (new token t, head h) of sequence b and cached token j, whose value row is
+// its code row times the scale s_j of its page:
+//     z_j = scale s_j ([q_lat | q_rope][r] . code_j),    o_lat[r] = sum_j softmax(z)_j s_j code_j[0:512]
+// over the first seq_lens[b] - q_len + t + 1 tokens, then out[r] = W_UV[h] o_lat[r].
 //
-// CUDA-core form: a warp owns one head of one query token and walks a range of tokens in
-// groups of 32 staged in shared memory, with a running maximum and sum.
-#include <cuda_fp16.h>
+// The codes are MMA operands as they are (kind::f8f6f4, E4M3); nothing is dequantised.  The
+// other operand of each product keeps 16-bit precision as the sum of two E4M3 terms: with
+// hi = e4m3(x) and lo = e4m3(x - hi), hi + lo is within 2^-8 |x| of x (half a step of 4 bits
+// twice), which is a bf16 rounding.  Two 8-bit products cost what one 16-bit product does.
+//
+// Tokens are the MMA's M.  A tile is 128 tokens (two pages); a group is R <= 64 query rows:
+//     S^T [128 tokens x 2R]  = codes [128 x 576] . [q_hi | q_lo]^T      (both terms in one product)
+//     O^T [4 x 128 latents x R] += codes^T [512 x 128] . P [128 x R]    (hi and lo)
+// so the codes are the A operand of both, K-major for the scores and MN-major for O, from the
+// one copy in shared memory; 64 rows' O takes 256 TMEM columns, two score buffers the other
+// 256, and a CTA needs no other CTA's scores.  A thread of the softmax holds one token and R/2
+// rows: P goes to shared memory in the layout the product reads, sums stay per thread until
+// the end of a piece, and the only thing the token lanes must agree on is each row's
+// reference M (below).
+//
+// The reference.  p = 2^(z' - M) must fit E4M3 (<= 448) and must not sink into its subnormals
+// (step 2^-9), so M follows the scores in both directions: it is set so that the tile's
+// largest p is 2^5, and set anew (O and the sums rescaled) when a tile's largest p leaves
+// [1, 2^8.5].  A one-sided running maximum, enough for a wider type, would leave everything
+// behind one dominating token to the subnormals.  The pages' scales ride on the
+// probabilities: z' = z + log2(s_j / s_ref) with s_ref the piece's first page's scale.
 #include <math.h>
 
 #include "decode_q8.cuh"
 #include "paged_plan.h"
+#include "tc_common.cuh"
 
 namespace mla {
 namespace q8 {
 
 namespace {
 
-constexpr int kDc = 512, kRow = 576;
-constexpr int kGroup = 32, kWarps = 8;
+constexpr int kDc = 512, kDr = 64, kRow = 576;
+constexpr int kT = 128;                       // tokens per tile
+constexpr int kChunkBytes = kT * 128;         // 128 latent columns of a tile (128-byte swizzle)
+constexpr int kRopeBytes = kT * kDr;          // the rotary columns of a tile (64-byte swizzle)
+constexpr int kThreads = 320;                 // TMA warp, MMA warp, 8 softmax warps
+constexpr int kPieceCost = 1;                 // cost units of a piece's query load and epilogue, in tiles
+constexpr int kMaxSib = 8;
+constexpr float kTopLog2 = 8.5f;              // p <= 2^8.5
+constexpr float kSetLog2 = 5.f;               // a new reference puts the tile's largest p here
+constexpr float kFarLog2 = 64.f;              // how far below its highest value a reference may go
 
-__global__ void __launch_bounds__(32 * kWarps)
-decode_split_kernel(const Problem p, const float* __restrict__ q_lat, const __nv_bfloat16* __restrict__ q_rope, int ns,
-                    float* __restrict__ part_o, float* __restrict__ part_ml, DevErr err) {
-    extern __shared__ float sm[];
-    constexpr int ld = kRow + 1;
-    float* tile = sm;                // [kGroup][ld] values
-    float* qs = sm + kGroup * ld;    // [kWarps][kRow]
-    const int v = blockIdx.x, split = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = v / p.q_len, t = v % p.q_len, h = blockIdx.z * kWarps + warp, NV = p.B * p.q_len;
-    int len = p.seq_lens[b];
-    if (len < 0 || (long long)len > (long long)p.max_blocks * kPageRows) {
-        if (threadIdx.x == 0) latch(err, kErrOutOfRange, b);
-        len = 0;
+// Shared memory: NC chunk slots, NR slots that hold a tile's rotary columns and then its P
+// (hi and, for R <= 32, lo), P's lo term (R = 64), the group's queries.
+template <int R> struct Cfg {
+    static constexpr int HC = R / 2;                     // rows per softmax thread
+    static constexpr bool kTwoPass = R == 64;            // P hi and lo as two products (one accumulator)
+    static constexpr int NP = kTwoPass ? R : 2 * R;      // N of an O product
+    static constexpr int NC = R == 64 ? 8 : R == 32 ? 10 : 11;
+    static constexpr int NR = 2;
+    static constexpr int kLoBytes = kTwoPass ? kRopeBytes : 0;
+    static constexpr int kQBytes = 2 * R * kRow;
+    static constexpr uint32_t kColO = 4 * R;
+    static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
+    static constexpr int kMisc = 3072;
+    static constexpr int kSmem = NC * kChunkBytes + NR * kRopeBytes + kLoBytes + kQBytes + kMisc;
+    static_assert(kColO + 4 * NP <= kTmemCols, "TMEM columns");
+    static_assert(kSmem <= 232448, "shared memory over the 227 KB limit");
+};
+
+// tcgen05.mma kind::f8f6f4, both operands in shared memory
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// E4M3 x E4M3 -> fp32
+constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major, int b_mn_major) {
+    return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+// MN-major operand in 64-byte-swizzled atoms: 64 one-byte MN elements per row, 8 K-rows per
+// 512-byte atom (N <= 64: one atom wide)
+__device__ __forceinline__ uint64_t desc_mnmajor_sw64(uint32_t saddr) { return ptx::smem_desc(saddr, 512, 512, 4); }
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { ptx::tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { ptx::tmem_st32(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) { ptx::tmem_st16(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {   // flushes results below 2^-126
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two values -> two E4M3 codes, `lo` in the low byte (nearest even, saturating, NaN kept)
+__device__ __forceinline__ uint32_t e4m3x2_f32(float lo, float hi) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t h2) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t code2) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)code2));
+    return h;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ---------------------------------------------------------------- work split
+// As in the other decode kernels: the tiles of all sequences, in order, are cut into equal
+// ranges; a range may hold pieces of several sequences.  A virtual sequence is a sequence
+// whose G groups are walked side by side by G neighbouring CTAs ("siblings": the pages then
+// come from HBM once), or, past kMaxSib groups, one (sequence, group) pair.
+struct Src {
+    const int32_t* seq_lens;
+    int max_blocks;
+    Shape s;
+    __device__ int raw_len(int b) const {
+        const int L = seq_lens[b];
+        return (L < 0 || (long long)L > (long long)max_blocks * kPageRows) ? -1 : L;
     }
-    const int keys = max(0, len - (p.q_len - 1 - t));
-    const int chunk = (keys + ns - 1) / ns;
-    const int j0 = min(keys, split * chunk), j1 = min(keys, j0 + chunk);
-    for (int i = threadIdx.x; i < kWarps * kRow; i += blockDim.x) {
-        const int hh = blockIdx.z * kWarps + i / kRow, c = i % kRow;
-        const long long r = (long long)v * p.H + hh;
-        qs[i] = hh >= p.H ? 0.f : c < kDc ? q_lat[r * kDc + c] : to_f(q_rope[r * (kRow - kDc) + c - kDc]);
+    __device__ int len(int b) const { return max(raw_len(b), 0); }
+    __device__ int first_token(int g) const { return g * s.R / s.H; }
+    __device__ int last_token(int g) const { return (min((g + 1) * s.R, s.q_len * s.H) - 1) / s.H; }
+    // keys of new token t of a sequence with L tokens
+    __device__ int keys(int L, int t) const { return L - (s.q_len - 1 - t); }
+    __device__ int vseqs() const { return s.sib > 1 ? s.B : s.B * s.G; }
+    __device__ int vlen(int i) const {
+        if (s.sib > 1) return len(i);
+        return max(keys(len(i / s.G), last_token(i % s.G)), 0);
     }
-    float m = -INFINITY, l = 0.f, acc[kDc / 32];
-#pragma unroll
-    for (int i = 0; i < kDc / 32; ++i) acc[i] = 0.f;
-    for (int jb = j0; jb < j1; jb += kGroup) {
-        const int nt = min(kGroup, j1 - jb);
-        __syncthreads();
-        for (int r = warp; r < nt; r += kWarps) {
-            const int j = jb + r;
-            const long long page = p.block_table[(long long)b * p.max_blocks + j / kPageRows];
-            const bool good = page >= 0 && page < p.num_pages;
-            if (!good && lane == 0) latch(err, kErrOutOfRange, b);
-            const uint8_t* src = p.codes + ((good ? page : 0) * kPageRows + j % kPageRows) * kRow;
-            const float s = good ? p.scales[page] : 0.f;
-            for (int c = 2 * lane; c < kRow; c += 64) {
-                uint32_t h2;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(*(const unsigned short*)(src + c)));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                tile[r * ld + c] = good ? f.x * s : 0.f;
-                tile[r * ld + c + 1] = good ? f.y * s : 0.f;
+};
+
+__device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kT - 1) / kT : 0; }
+__device__ __forceinline__ long long cost_of(int n) { return n > 0 ? n + kPieceCost : 0; }
+
+// tiles [j0, j1) of group g of sequence b
+struct Seg {
+    int b, item, g, j0, j1, len, kmin, kmax, slot;
+};
+struct SegIter {
+    Src src;
+    int nv, sib_idx, cta;
+    long long lo, hi, cs;
+    int i;
+    __device__ bool next(Seg& s) {
+        while (i < nv && cs < hi) {
+            const int ii = i++;
+            const int n = tiles_of(src.vlen(ii));
+            const long long f = cs + kPieceCost;
+            cs += cost_of(n);
+            if (n == 0) continue;
+            s.b = src.s.sib > 1 ? ii : ii / src.s.G;
+            s.g = src.s.sib > 1 ? sib_idx : ii % src.s.G;
+            s.item = s.b * src.s.G + s.g;
+            s.len = src.len(s.b);
+            s.kmin = src.keys(s.len, src.first_token(s.g));
+            s.kmax = src.keys(s.len, src.last_token(s.g));
+            s.j0 = lo > f ? (int)(lo - f) : 0;
+            s.j1 = (int)min(hi - f, (long long)tiles_of(s.kmax));
+            if (s.j0 < s.j1) {
+                s.slot = s.j0 == 0 ? s.item : src.s.B * src.s.G + cta;
+                return true;
             }
         }
+        return false;
+    }
+};
+
+__device__ __forceinline__ void fail(DevErr err, volatile int* abort_flag, int where) {
+    latch(err, kErrTimeout, (long long)where * 1000000 + blockIdx.x);
+    *abort_flag = 1;
+}
+
+// ------------------------------------------------------------------ attention
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope, const Src src,
+            const int32_t* __restrict__ block_table, const float* __restrict__ scales, long long num_pages,
+            float scale_log2, const Ws ws, const DevErr err) {
+    using C = Cfg<R>;
+    constexpr int HC = C::HC, NC = C::NC, NR = C::NR;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (ptx::smem_u32(smem) & 1023) {   // uniform: leave before any barrier
+        if (threadIdx.x == 0) latch(err, kErrTimeout, 9000000);
+        return;
+    }
+    uint8_t* chunks = smem;
+    uint8_t* ropes = chunks + NC * kChunkBytes;
+    uint8_t* plo = ropes + NR * kRopeBytes;
+    uint8_t* qimg = plo + C::kLoBytes;
+    float* qs = (float*)(qimg + C::kQBytes);            // [2][R] row scales of this piece's and the next's queries
+    float4* red = (float4*)(qs + 2 * 64);               // [2][32] per row, one value per token quarter
+    float* tops = (float*)(red + 64);                   // [2][4][32] each warp's highest references; sums at a piece's end
+    uint64_t* bars = (uint64_t*)(tops + 256);
+    uint64_t *chunk_full = bars, *chunk_empty = bars + 11, *rope_full = bars + 22, *rope_empty = bars + 24;
+    uint64_t *q_full = bars + 26, *s_full = bars + 27, *s_free = bars + 29, *p_ready = bars + 31;
+    uint64_t *lo_free = bars + 33, *o_done = bars + 34, *half_bar = bars + 36, *drain = bars + 38;
+    float* page_scale = (float*)(bars + 40);            // [4 tiles][2 pages]
+    uint32_t* flags = (uint32_t*)(page_scale + 8);      // [2 tiles][2 halves][4]
+    uint32_t* tmem_slot = flags + 16;
+    volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+    float* out_scale = (float*)(tmem_slot + 2);         // [2 halves][4] largest page scale a warp saw
+    static_assert(2 * 64 * 4 + 64 * 16 + 256 * 4 + 40 * 8 + 8 * 4 + 16 * 4 + 8 + 8 * 4 <= C::kMisc, "barrier area");
+    // the planning's scratch lies where the reductions come later
+    long long* plan_wsum = (long long*)red;             // [10]
+    long long* plan_first = plan_wsum + 10;             // [2]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NC; ++i) {
+            ptx::mbar_init(&chunk_full[i], 1);
+            ptx::mbar_init(&chunk_empty[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            ptx::mbar_init(&rope_full[i], 1);
+            ptx::mbar_init(&rope_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s_full[i], 1);
+            ptx::mbar_init(&s_free[i], 256);
+            ptx::mbar_init(&p_ready[i], 256);
+            ptx::mbar_init(&half_bar[i], 4);
+            ptx::mbar_init(&o_done[i], 1);
+        }
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(lo_free, 1);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::tma_prefetch(&tm_lat);
+        ptx::tma_prefetch(&tm_rope);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(tmem_slot, C::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (threadIdx.x == 0) pdl_trigger();
+
+    // ---- planning: total cost, then the virtual sequence that holds this CTA's first unit.
+    // The call's first kernel waits for all earlier work before it lets this one launch, so
+    // lengths, table and cache are final.
+    constexpr int kWarps = kThreads / 32;
+    const int nv = src.vseqs(), ranges = src.s.ctas / src.s.sib;
+    const int range = (int)blockIdx.x / src.s.sib, sib_idx = (int)blockIdx.x % src.s.sib;
+    long long total = 0;
+    {
+        long long mine = 0;
+        for (int i = threadIdx.x; i < nv; i += kThreads) mine += cost_of(tiles_of(src.vlen(i)));
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b < src.s.B; b += kThreads)
+                if (src.raw_len(b) < 0) latch(err, kErrOutOfRange, b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) plan_wsum[warp] = mine;
+        if (threadIdx.x == 0) {
+            plan_first[0] = nv;
+            plan_first[1] = 0;
+        }
+        ptx::tc_fence_before();
         __syncthreads();
-        if (h >= p.H) continue;
-        float s = -INFINITY;
-        if (lane < nt) {
-            float a = 0.f;
-            for (int c = 0; c < kRow; ++c) a = fmaf(qs[warp * kRow + c], tile[lane * ld + c], a);
-            s = a * p.scale;
-        }
-        float mn = s;
+        ptx::tc_fence_after();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mn = fmaxf(m, mn);
-        const float alpha = m == -INFINITY ? 0.f : expf(m - mn), w = lane < nt ? expf(s - mn) : 0.f;
-        float sum = w;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        l = l * alpha + sum;
-#pragma unroll
-        for (int i = 0; i < kDc / 32; ++i) acc[i] *= alpha;
-        for (int r = 0; r < nt; ++r) {
-            const float wr = __shfl_sync(0xffffffffu, w, r);
-#pragma unroll
-            for (int i = 0; i < kDc / 32; ++i) acc[i] = fmaf(wr, tile[r * ld + lane + 32 * i], acc[i]);
-        }
-        m = mn;
+        for (int i = 0; i < kWarps; ++i) total += plan_wsum[i];
+        __syncthreads();
     }
-    if (h >= p.H) return;
-    const long long at = ((long long)split * NV + v) * p.H + h;
+    const long long per = total > 0 ? (total + ranges - 1) / ranges : 1;
+    const long long lo = range < ranges ? min(total, range * per) : total, hi = min(total, lo + per);
+    if (blockIdx.x == 0 && threadIdx.x == 0) ws.plan[0] = per;
+    if (lo < total || blockIdx.x == 0) {
+        long long carry = 0;
+        for (int c0 = 0; c0 < nv; c0 += kThreads) {
+            const int i = c0 + (int)threadIdx.x;
+            const long long cb = i < nv ? cost_of(tiles_of(src.vlen(i))) : 0;
+            long long incl = cb;
 #pragma unroll
-    for (int i = 0; i < kDc / 32; ++i) part_o[at * kDc + lane + 32 * i] = acc[i];
-    if (lane == 0) {
-        // a NaN sum (a NaN in a row that counts) as an infinite one, which the merge keeps: O is NaN
-        part_ml[2 * at] = isnan(l) && m == -INFINITY ? 0.f : m;
-        part_ml[2 * at + 1] = isnan(l) ? INFINITY : l;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) plan_wsum[warp] = incl;
+            __syncthreads();
+            long long before = carry, chunk = 0;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const long long v = plan_wsum[k];
+                before += k < warp ? v : 0;
+                chunk += v;
+            }
+            const long long cs = before + incl - cb;
+            if (i < nv) {
+                if (cb > 0 && cs <= lo && lo < cs + cb) {   // unique: the region that holds lo
+                    plan_first[0] = i;
+                    plan_first[1] = cs;
+                }
+                if (blockIdx.x == 0) ws.plan[1 + i] = cs;   // for the merge
+            }
+            carry += chunk;
+            __syncthreads();
+        }
     }
+    SegIter it{src, nv, sib_idx, (int)blockIdx.x, lo, hi, plan_first[1], (int)plan_first[0]};
+    const uint32_t tmem = *tmem_slot;
+    __syncthreads();   // plan_first is read before red is written
+
+    Seg sg;
+    if (warp == 0) {
+        // ---------------------------------------------------------- TMA producer
+        // lane l holds the page (and its scale) of block base + l of the sequence
+        const uint64_t policy = src.s.G > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+        const long long none = num_pages * kPageRows;   // a box past the last row reads zeros
+        uint32_t g = 0, cn = 0;                         // tiles, chunks requested
+        bool ok = true;
+        while (ok && !*abort_flag && it.next(sg)) {
+            const int blocks = (sg.len + kPageRows - 1) / kPageRows;
+            long long row = none;
+            float sc = 0.f;
+            for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+                const int at = (j - sg.j0) & 15;
+                if (at == 0) {
+                    const int blk = 2 * j + lane;
+                    const long long page = blk < blocks ? block_table[(long long)sg.b * src.max_blocks + blk] : -1;
+                    const bool good = page >= 0 && page < num_pages;
+                    row = good ? page * kPageRows : none;
+                    sc = good ? scales[page] : 0.f;
+                    // only the pages this piece reads are its to report
+                    if (!good && blk < blocks && blk < 2 * sg.j1) latch(err, kErrOutOfRange, sg.b);
+                }
+                const int r0 = (int)__shfl_sync(0xffffffffu, row, 2 * at), r1 = (int)__shfl_sync(0xffffffffu, row, 2 * at + 1);
+                const float s0 = __shfl_sync(0xffffffffu, sc, 2 * at), s1 = __shfl_sync(0xffffffffu, sc, 2 * at + 1);
+                if (lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c, ++cn) {
+                        const uint32_t slot = cn % NC, use = cn / NC;
+                        if (ok && use > 0 && !ptx::mbar_wait(&chunk_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
+                        if (!ok) break;
+                        uint8_t* dst = chunks + slot * kChunkBytes;
+                        ptx::mbar_expect_tx(&chunk_full[slot], kChunkBytes);
+                        ptx::tma_load_2d_hint(dst, &tm_lat, &chunk_full[slot], 128 * c, r0, policy);
+                        ptx::tma_load_2d_hint(dst + kChunkBytes / 2, &tm_lat, &chunk_full[slot], 128 * c, r1, policy);
+                    }
+                    const uint32_t slot = g % NR, use = g / NR;
+                    if (ok && use > 0 && !ptx::mbar_wait(&rope_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
+                    if (ok) {
+                        page_scale[2 * (g & 3)] = s0;
+                        page_scale[2 * (g & 3) + 1] = s1;
+                        uint8_t* dst = ropes + slot * kRopeBytes;
+                        ptx::mbar_expect_tx(&rope_full[slot], kRopeBytes);
+                        ptx::tma_load_2d_hint(dst, &tm_rope, &rope_full[slot], kDc, r0, policy);
+                        ptx::tma_load_2d_hint(dst + kRopeBytes / 2, &tm_rope, &rope_full[slot], kDc, r1, policy);
+                    } else {
+                        --g;   // this tile's rotary columns were not requested
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) fail(err, abort_flag, 11);
+            // loads still in flight (after an abort) land before the CTA leaves
+            for (uint32_t k = 0; k < (uint32_t)NC && k < cn; ++k)
+                ptx::mbar_wait(&chunk_full[(cn - 1 - k) % NC], ((cn - 1 - k) / NC) & 1, nullptr);
+            for (uint32_t k = 0; k < (uint32_t)NR && k < g; ++k)
+                ptx::mbar_wait(&rope_full[(g - 1 - k) % NR], ((g - 1 - k) / NR) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // Event-driven: O of the oldest tile whose P is written, else the next score step (one
+        // 128-column chunk, or the rotary columns) whose data has landed.  Scores run at most
+        // two tiles ahead of O.
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_e4m3(128, 2 * R, 0, 0);
+            constexpr uint32_t idesc_o = idesc_e4m3(128, C::NP, 1, 1);
+            const uint32_t chunk0 = ptx::smem_u32(chunks), rope0 = ptx::smem_u32(ropes), lo0 = ptx::smem_u32(plo),
+                           q0 = ptx::smem_u32(qimg);
+            SegIter its = it;
+            Seg ss;
+            bool s_have = !*abort_flag && its.next(ss), o_have = !*abort_flag && it.next(sg);
+            int s_j = s_have ? ss.j0 : 0, o_j = o_have ? sg.j0 : 0, s_c = 0;
+            uint32_t s_g = 0, o_g = 0, piece = 0, idle = 0;
+            bool ok = true;
+            while (o_have) {
+                if (o_g < s_g && ptx::mbar_test(&p_ready[o_g & 1], (o_g >> 1) & 1)) {
+                    ptx::tc_fence_after();
+                    const uint32_t acc0 = o_j != sg.j0;
+                    const uint32_t p_hi = rope0 + (o_g % NR) * kRopeBytes;
+                    if (C::kTwoPass) {   // the lo terms first: their buffer is free for the next tile sooner
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t a = chunk0 + ((4 * o_g + c) % NC) * kChunkBytes;
+#pragma unroll
+                            for (int k = 0; k < kT / 32; ++k)
+                                mma_f8(tmem + C::kColO + c * C::NP, ptx::desc_mnmajor_sw128(a + 4096 * k, kChunkBytes),
+                                       desc_mnmajor_sw64(lo0 + 2048 * k), idesc_o, acc0 | (k > 0));
+                        }
+                        ptx::mma_commit(lo_free);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t slot = (4 * o_g + c) % NC, a = chunk0 + slot * kChunkBytes;
+#pragma unroll
+                        for (int k = 0; k < kT / 32; ++k)
+                            mma_f8(tmem + C::kColO + c * C::NP, ptx::desc_mnmajor_sw128(a + 4096 * k, kChunkBytes),
+                                   desc_mnmajor_sw64(p_hi + 2048 * k), idesc_o, C::kTwoPass || acc0 | (k > 0));
+                        ptx::mma_commit(&chunk_empty[slot]);
+                    }
+                    ptx::mma_commit(&o_done[o_g & 1]);
+                    ptx::mma_commit(&rope_empty[o_g % NR]);
+                    ++o_g;
+                    if (++o_j == sg.j1) {
+                        o_have = it.next(sg);
+                        o_j = o_have ? sg.j0 : 0;
+                    }
+                    idle = 0;
+                    continue;
+                }
+                if (s_have && s_g < o_g + 2) {
+                    bool ready;
+                    if (s_c < 4) {
+                        const uint32_t cn = 4 * s_g + s_c;
+                        ready = ptx::mbar_test(&chunk_full[cn % NC], (cn / NC) & 1);
+                        if (s_c == 0)
+                            ready = ready && (s_g < 2 || ptx::mbar_test(&s_free[s_g & 1], ((s_g >> 1) - 1) & 1)) &&
+                                    (s_j != ss.j0 || ptx::mbar_test(q_full, piece & 1));
+                    } else {
+                        ready = ptx::mbar_test(&rope_full[s_g % NR], (s_g / NR) & 1);
+                    }
+                    if (ready) {
+                        ptx::tc_fence_after();
+                        const uint32_t d = tmem + (s_g & 1) * (2 * R);
+                        if (s_c < 4) {
+                            const uint32_t a = chunk0 + ((4 * s_g + s_c) % NC) * kChunkBytes, b = q0 + s_c * (2 * R * 128);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8(d, ptx::desc_kmajor_sw128(a + 32 * k), ptx::desc_kmajor_sw128(b + 32 * k), idesc_s,
+                                       (s_c | k) != 0);
+                            ++s_c;
+                        } else {
+                            const uint32_t a = rope0 + (s_g % NR) * kRopeBytes, b = q0 + 4 * (2 * R * 128);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                mma_f8(d, ptx::desc_kmajor_sw64(a + 32 * k), ptx::desc_kmajor_sw64(b + 32 * k), idesc_s, 1);
+                            ptx::mma_commit(&s_full[s_g & 1]);
+                            s_c = 0;
+                            ++s_g;
+                            if (++s_j == ss.j1) {
+                                s_have = its.next(ss);
+                                s_j = s_have ? ss.j0 : 0;
+                                ++piece;
+                            }
+                        }
+                        idle = 0;
+                        continue;
+                    }
+                }
+                // polls do not block here: 16 of them count as one of the other waits'
+                if (++idle > (ptx::g_wait_limit << 4) || *abort_flag) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok) fail(err, abort_flag, 12);
+            ptx::mma_commit(drain);
+            if (!ptx::mbar_wait(drain, 0, nullptr)) fail(err, abort_flag, 14);
+        }
+    } else {
+        // ------------------------------------------------- softmax and epilogue
+        const int quad = warp & 3, half = warp >= 6 ? 1 : 0;
+        const int tok = 32 * quad + lane;                       // token of the tile = TMEM lane
+        const int c0 = half * HC;                               // first row of this thread
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * quad) << 16);
+        const bool loader = warp == 2 && lane == 0;             // requests the queries
+        bool ok = true;
+        auto uwait = [&](uint64_t* bar, uint32_t parity) {      // warp-uniform result
+            return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag));
+        };
+        uint32_t meets = 0;
+        auto meet = [&]() {   // the four warps that share this half's rows
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&half_bar[half]);
+            if (!uwait(&half_bar[half], meets & 1)) ok = false;
+            ++meets;
+        };
+        auto load_q = [&](const Seg& s, uint32_t piece) {
+            ptx::mbar_expect_tx(q_full, C::kQBytes + R * 4);
+            const uint8_t* from = ws.q_img + (size_t)s.item * C::kQBytes;
+            for (int o = 0; o < C::kQBytes; o += C::kQBytes / 4)
+                ptx::bulk_load(qimg + o, from + o, C::kQBytes / 4, q_full);
+            ptx::bulk_load(qs + (piece & 1) * 64, ws.q_scale + (size_t)s.item * R, R * 4, q_full);
+        };
+        pdl_wait();   // the queries come from the previous kernel of this call
+        Seg nxt;
+        bool have = it.next(sg);
+        uint32_t piece = 0, g = 0, q_loads = 0;
+        if (loader && have) {
+            load_q(sg, 0);
+            ++q_loads;
+        }
+        float M[HC], l[HC];
+        while (have && ok) {
+            const bool more = it.next(nxt);
+            float s_ref = 1.f, s_top = 0.f;
+            const float* qsp = qs + (piece & 1) * 64 + c0;
+            for (int j = sg.j0; j < sg.j1; ++j, ++g) {
+                const bool first = j == sg.j0;
+                if (first && !uwait(q_full, piece & 1)) { ok = false; break; }   // row scales
+                if (!uwait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }   // page scales
+                if (!uwait(&s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
+                // O of tile g - 2 is done (its P lay where this tile's goes); every phase of the
+                // barrier is waited for, so that a later wait cannot take an older one for its own
+                if (g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
+                ptx::tc_fence_after();
+                float arg[HC];
+                {
+                    uint32_t a[HC], b[HC];
+                    tmem_ld(lane_addr + (g & 1) * (2 * R) + c0, a);
+                    tmem_ld(lane_addr + (g & 1) * (2 * R) + R + c0, b);
+                    ptx::tmem_wait_ld();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&s_free[g & 1]);
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) arg[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+                }
+                if (loader && j + 1 == sg.j1 && more) {
+                    // The piece's last scores are done with its queries.  Every warp has read
+                    // these scores, so it has seen q_full of this piece and is done with the
+                    // row scales of the one before.
+                    if (!ptx::mbar_wait(&s_free[g & 1], (g >> 1) & 1, abort_flag)) {
+                        fail(err, abort_flag, 15);
+                    } else {
+                        load_q(nxt, piece + 1);
+                        ++q_loads;
+                    }
+                }
+                float s = page_scale[2 * (g & 3) + (quad >> 1)];
+                if (first) {
+                    const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
+                    s_ref = sa != 0.f ? sa : sb != 0.f ? sb : 1.f;
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) M[i] = 0.f, l[i] = 0.f;
+                }
+                s_top = fmaxf(s_top, s);
+                if (s == 0.f) s = s_ref;   // no page: zero rows
+                const bool same = s == s_ref;
+                const float kt = scale_log2 * s, shift = same ? 0.f : log2f(s) - log2f(s_ref), back = same ? 1.f : s_ref / s;
+#pragma unroll
+                for (int i = 0; i < HC; i += 4) {
+                    const float4 f = *(const float4*)(qsp + i);
+                    arg[i] = fmaf(arg[i], f.x * kt, shift - M[i]);
+                    arg[i + 1] = fmaf(arg[i + 1], f.y * kt, shift - M[i + 1]);
+                    arg[i + 2] = fmaf(arg[i + 2], f.z * kt, shift - M[i + 2]);
+                    arg[i + 3] = fmaf(arg[i + 3], f.w * kt, shift - M[i + 3]);
+                }
+                const bool edge = (j + 1) * kT > sg.kmin;   // some row does not see the whole tile
+                if (edge) {
+                    const int at = j * kT + tok;
+                    if (sg.kmin == sg.kmax) {
+                        if (at >= sg.kmax) {
+#pragma unroll
+                            for (int i = 0; i < HC; ++i) arg[i] = -INFINITY;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < HC; ++i)
+                            if (at >= src.keys(sg.len, (sg.g * R + c0 + i) / src.s.H)) arg[i] = -INFINITY;
+                    }
+                }
+                // Does every row keep its reference?  Sign bits of the arguments, anded over the
+                // tile's tokens, name the rows whose largest p is below 1; any argument past the
+                // top sends the warp's word to "all".
+                {
+                    uint32_t low = 0;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) {
+                        low = __funnelshift_l(__float_as_uint(arg[i]), low, 1);
+                        top = fmaxf(top, arg[i]);
+                    }
+                    low = __reduce_and_sync(0xffffffffu, low);
+                    if (__any_sync(0xffffffffu, top > kTopLog2)) low = 0xffffffffu;
+                    if (lane == 0) flags[(g & 1) * 8 + half * 4 + quad] = low;
+                }
+                meet();
+                if (!ok) break;
+                const uint4 fl = *(const uint4*)(flags + (g & 1) * 8 + half * 4);
+                const bool over = fl.x == 0xffffffffu || fl.y == 0xffffffffu || fl.z == 0xffffffffu || fl.w == 0xffffffffu;
+                if (first || over || (fl.x & fl.y & fl.z & fl.w) != 0) {
+                    float keep = -INFINITY;   // lane i: this warp's largest z' of row c0 + i
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) {
+                        float v = arg[i] + M[i];
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                        if (lane == i) keep = v;
+                    }
+                    if (lane < HC) ((float*)red)[(half * 32 + lane) * 4 + quad] = keep;
+                    meet();
+                    if (!ok) break;
+                    bool moved = false;
+                    float alpha[HC];
+                    float* my_top = tops + (half * 4 + quad) * 32;
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) {
+                        const float4 v = red[half * 32 + i];
+                        const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+                        float m = M[i];
+                        if (mx > -INFINITY && (first || mx - m > kTopLog2 || mx < m)) {
+                            m = mx - kSetLog2;
+                            if (!first) m = fmaxf(m, my_top[i] - kFarLog2);
+                        }
+                        alpha[i] = ex2(M[i] - m);
+                        arg[i] += M[i] - m;
+                        moved = moved || (!first && m != M[i]);
+                        M[i] = m;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < HC; ++i)
+                        if (lane == i) my_top[i] = first ? M[i] : fmaxf(my_top[i], M[i]);
+                    __syncwarp();
+                    if (moved) {   // the same for all token lanes
+                        if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < HC; ++i) l[i] *= alpha[i];
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll 1
+                            for (int term = 0; term < C::NP / R; ++term) {
+                                uint32_t r[HC];
+                                const uint32_t ad = lane_addr + C::kColO + c * C::NP + term * R + c0;
+                                tmem_ld(ad, r);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < HC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha[i]);
+                                tmem_st(ad, r);
+                            }
+                        ptx::tmem_wait_st();
+                    }
+                }
+                // P in two E4M3 terms; the sums take the unrounded p
+                uint32_t hi8[HC / 4], lo8[HC / 4];
+#pragma unroll
+                for (int i = 0; i < HC; i += 4) {
+                    uint32_t h[2], t[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float p0 = ex2(arg[i + 2 * q]), p1 = ex2(arg[i + 2 * q + 1]);
+                        l[i + 2 * q] = fmaf(p0, back, l[i + 2 * q]);
+                        l[i + 2 * q + 1] = fmaf(p1, back, l[i + 2 * q + 1]);
+                        const uint32_t v = ptx::pack_f16(p0, p1);
+                        h[q] = e4m3x2_f16(v);
+                        t[q] = e4m3x2_f16(hsub2(v, f16x2_of_e4m3(h[q])));
+                    }
+                    hi8[i / 4] = h[0] | (h[1] << 16);
+                    lo8[i / 4] = t[0] | (t[1] << 16);
+                }
+                // row tok of P: 64 bytes, 16-byte unit u at u ^ (tok / 2 % 4)
+                uint8_t* prow = ropes + (g % NR) * kRopeBytes + tok * 64;
+                const int sw = (tok >> 1) & 3;
+                if (C::kTwoPass) {
+                    if (g > 0 && !uwait(lo_free, (g - 1) & 1)) { ok = false; break; }
+                    uint8_t* lrow = plo + tok * 64;
+#pragma unroll
+                    for (int u = 0; u < HC / 16; ++u) {
+                        const int at = ((half * 2 + u) ^ sw) << 4;
+                        *(uint4*)(prow + at) = make_uint4(hi8[4 * u], hi8[4 * u + 1], hi8[4 * u + 2], hi8[4 * u + 3]);
+                        *(uint4*)(lrow + at) = make_uint4(lo8[4 * u], lo8[4 * u + 1], lo8[4 * u + 2], lo8[4 * u + 3]);
+                    }
+                } else if (R == 32) {
+                    *(uint4*)(prow + ((half ^ sw) << 4)) = make_uint4(hi8[0], hi8[1], hi8[HC / 8], hi8[HC / 4 - 1]);
+                    *(uint4*)(prow + (((2 + half) ^ sw) << 4)) = make_uint4(lo8[0], lo8[1], lo8[HC / 8], lo8[HC / 4 - 1]);
+                } else {
+                    *(uint2*)(prow + ((0 ^ sw) << 4) + 8 * half) = make_uint2(hi8[0], hi8[1]);
+                    *(uint2*)(prow + ((1 ^ sw) << 4) + 8 * half) = make_uint2(lo8[0], lo8[1]);
+                }
+                if (edge) {
+                    // Rows that some row of the group must not see may hold NaN codes (what lies
+                    // behind the sequence's end, a later token's row), and 0 x NaN is NaN: those
+                    // codes become 0.  A row that does see them has NaN scores already.
+                    const int n0 = max(sg.kmin - j * kT, 0);
+                    const int tid = threadIdx.x - 64;   // 0 .. 255
+                    for (int e = tid; e < (kT - n0) * 32; e += 256) {
+                        const int r = n0 + (e >> 5), c = (e >> 3) & 3, u = e & 7;
+                        uint4* at = (uint4*)(chunks + ((4 * g + c) % NC) * kChunkBytes + r * 128) + u;
+                        uint4 v = *at;
+                        v.x &= ~__vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        v.y &= ~__vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        v.z &= ~__vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        v.w &= ~__vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        *at = v;
+                    }
+                }
+                ptx::fence_proxy_async_smem();   // read by the tensor cores
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&p_ready[g & 1]);
+            }
+            if (!ok) break;
+            // ---- the piece's sums over all tokens, then its normalised output
+            // after step o, a lane holds the sums over 32 / o lanes of the rows whose bits match its own
+#pragma unroll
+            for (int w = HC / 2, o = 16; o > 0; o >>= 1, w = w > 0 ? w / 2 : 0) {
+                if (w > 0) {
+                    const bool up = (lane & o) != 0;
+#pragma unroll
+                    for (int i = 0; i < HC / 2; ++i)
+                        if (i < w) {
+                            const float mine = up ? l[i + w] : l[i], give = up ? l[i] : l[i + w];
+                            l[i] = mine + __shfl_xor_sync(0xffffffffu, give, o);
+                        }
+                } else {
+                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+                }
+            }
+            // row held by this lane: the lane bits from 16 down, as many as HC has
+            const int my_row = lane >> (HC == 32 ? 0 : HC == 16 ? 1 : 2);
+            float* sums = tops + half * 128;   // [4 quarters][32]
+            __syncwarp();
+            sums[quad * 32 + my_row] = l[0];
+            if (lane == 0) out_scale[half * 4 + quad] = s_top;
+            meet();
+            if (!ok) break;
+            const float* st4 = out_scale + half * 4;
+            const float s_out0 = fmaxf(fmaxf(st4[0], st4[1]), fmaxf(st4[2], st4[3]));
+            const float s_out = s_out0 > 0.f ? s_out0 : 1.f;
+            if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
+            ptx::tc_fence_after();
+            float f[HC];
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                const float t = (sums[i] + sums[32 + i]) + (sums[64 + i] + sums[96 + i]);
+                f[i] = t != 0.f ? (s_ref / s_out) / t : 0.f;
+                if (quad == 0 && lane == i) ws.part_ml[(size_t)sg.slot * R + c0 + i] = make_float4(M[i], t, s_out, 0.f);
+            }
+            __half* po = ws.part_o + ((size_t)sg.slot * R + c0) * kDc + tok;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[HC];
+                tmem_ld(lane_addr + C::kColO + c * C::NP + c0, r);
+                if (C::NP > R) {
+                    uint32_t r2[HC];
+                    tmem_ld(lane_addr + C::kColO + c * C::NP + R + c0, r2);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
+                } else {
+                    ptx::tmem_wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(__uint_as_float(r[i]) * f[i]);
+            }
+            ptx::tc_fence_before();
+            meet();   // the sums are read before the next piece's references come in their place
+            sg = nxt;
+            have = more;
+            ++piece;
+        }
+        if (!ok) fail(err, abort_flag, 13);
+        if (loader && q_loads > 0) ptx::mbar_wait(q_full, (q_loads - 1) & 1, nullptr);   // in flight after an abort
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) ptx::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ------------------------------------------------------------------ the queries
+// q_lat[v, h, :] = W_UK[h]^T q_nope[v, h, :] for 128 queries v = (b, t) of one head, as
+// D [128 queries x 512] = Q_h [128 x 128] . W_UK^T[h]^T, so that a query is a TMEM lane and the
+// four warps of a lane quarter hold its 512 values: the row [q_lat | q_rope] gets one
+// power-of-two scale that puts its largest value in (224, 448], and leaves as the two E4M3
+// terms in the shared-memory image the attention kernel loads whole.
+// One CTA per (head, 128 queries): the 128 KB of W_UK^T[h] bound it.
+constexpr int kAbsorbThreads = 512;
+constexpr int kAbsorbA = 2 * 128 * 128, kAbsorbB = 4 * 256 * 128;
+constexpr int kAbsorbSmem = kAbsorbA + kAbsorbB + 4 * 128 * 4 + 64 + 1024;
+
+// smallest e with amax <= 448 * 2^e (0 for 0), not below -100
+__device__ __forceinline__ int query_exponent(float amax) {
+    if (!(amax > 0.f)) return 0;
+    const uint32_t u = __float_as_uint(amax);
+    return max((int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0), -100);
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ void split_e4m3(const float (&x)[16], float inv, uint4& hi, uint4& lo) {
+    uint32_t h[8], t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+        h[i] = e4m3x2_f32(a, b);
+        const uint32_t f = f16x2_of_e4m3(h[i]);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+        t[i] = e4m3x2_f32(a - v.x, b - v.y);
+    }
+    hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    lo = make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
+}
+
+__global__ void __launch_bounds__(kAbsorbThreads, 1)
+absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_w,
+              const __nv_bfloat16* __restrict__ q_rope, const Shape s, const Ws ws, const DevErr err) {
+    extern __shared__ uint8_t absorb_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)absorb_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sA = smem, *sB = smem + kAbsorbA;
+    float* s_max = (float*)(sB + kAbsorbB);   // [4 column groups][128]
+    uint64_t* full = (uint64_t*)(s_max + 512);
+    uint64_t* d_full = full + 1;
+    uint32_t* tmem_slot = (uint32_t*)(d_full + 1);
+    const int h = blockIdx.x, v0 = blockIdx.y * 128, NV = s.B * s.q_len;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, cg = warp >> 2;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(full, 1);
+        ptx::mbar_init(d_full, 1);
+        ptx::fence_mbar_init();
+        ptx::mbar_expect_tx(full, kAbsorbA + kAbsorbB);
+        // the weights first: earlier kernels do not write them
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                ptx::tma_load_2d(sB + (2 * kc + n) * 32768, &tm_w, full, 64 * kc, h * kDc + 256 * n);
+        pdl_wait();      // all earlier work is done
+        pdl_trigger();   // only now may the next kernel launch
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc) ptx::tma_load_3d(sA + kc * 16384, &tm_q, full, 64 * kc, v0, h);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(tmem_slot, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 32) {
+        if (!ptx::mbar_wait(full, 0, nullptr)) {
+            latch(err, kErrTimeout, 9200000 + h);
+        } else {
+            ptx::tc_fence_after();
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, 256, 0, 0);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem + 256 * n, ptx::desc_kmajor_sw128(ptx::smem_u32(sA + kc * 16384) + 32 * k),
+                                    ptx::desc_kmajor_sw128(ptx::smem_u32(sB + (2 * kc + n) * 32768) + 32 * k), idesc,
+                                    (kc | k) != 0);
+        }
+        ptx::mma_commit(d_full);   // after a timeout nothing was issued and this completes at once
+    }
+    __syncwarp();
+    const int v = v0 + 32 * quad + lane;
+    const bool warp_on = v0 + 32 * quad < NV, on = v < NV;
+    const uint32_t src_col = tmem + ((uint32_t)(32 * quad) << 16) + 128 * cg;
+    // this warp group's 16 rotary columns; they may come from the previous kernel
+    pdl_wait();
+    float rope[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) rope[i] = 0.f;
+    if (on) {
+        const uint4* r = (const uint4*)(q_rope + ((size_t)v * s.H + h) * kDr + 16 * cg);
+        const uint4 a = r[0], b = r[1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            rope[2 * i] = __uint_as_float(w[i] << 16);
+            rope[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    const bool done = __all_sync(0xffffffffu, ptx::mbar_wait(d_full, 0, nullptr));
+    if (!done && lane == 0) latch(err, kErrTimeout, 9300000 + h);
+    ptx::tc_fence_after();
+    float amax = 0.f;
+    if (warp_on) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(rope[i]));
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld32(src_col + c, r);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(r[i])));
+        }
+    }
+    s_max[cg * 128 + 32 * quad + lane] = amax;
+    __syncthreads();
+    if (warp_on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, s_max[i * 128 + 32 * quad + lane]);
+        const int e = query_exponent(amax);
+        // an infinite query value must not saturate: times 0 it is NaN, as its scores are
+        const float inv = amax < INFINITY ? pow2i(-e) : 0.f;
+        const int R = s.R, b = v / s.q_len, t = v % s.q_len, row = t * s.H + h;
+        const size_t img = (size_t)2 * R * kRow, chunk = (size_t)2 * R * 128;
+        uint8_t* base = ws.q_img + ((size_t)b * s.G + row / R) * img;
+        const int rh = row % R, rl = R + rh;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld32(src_col + c, r);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[16 * q + i]);
+                uint4 hi, lo;
+                split_e4m3(x, inv, hi, lo);
+                const int u = c / 16 + q;
+                if (on) {
+                    *(uint4*)(base + cg * chunk + rh * 128 + ((u ^ (rh & 7)) << 4)) = hi;
+                    *(uint4*)(base + cg * chunk + rl * 128 + ((u ^ (rl & 7)) << 4)) = lo;
+                }
+            }
+        }
+        if (on) {
+            uint4 hi, lo;
+            split_e4m3(rope, inv, hi, lo);
+            uint8_t* rp = base + 4 * chunk;
+            *(uint4*)(rp + rh * 64 + ((cg ^ ((rh >> 1) & 3)) << 4)) = hi;
+            *(uint4*)(rp + rl * 64 + ((cg ^ ((rl >> 1) & 3)) << 4)) = lo;
+            if (cg == 0) ws.q_scale[((size_t)b * s.G + row / R) * R + rh] = pow2i(e);
+            // rows that pad a sequence's last group are zero: head h writes the h-th, (h + H)-th, ...
+            if (t == s.q_len - 1) {
+                for (int p = s.q_len * s.H + h; p < s.G * R; p += s.H) {
+                    const int ph = p % R, pl = R + ph;
+                    uint8_t* pb = ws.q_img + ((size_t)b * s.G + p / R) * img;
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    for (int u = 0; u < 8; ++u) {
+                        *(uint4*)(pb + cg * chunk + ph * 128 + 16 * u) = z;
+                        *(uint4*)(pb + cg * chunk + pl * 128 + 16 * u) = z;
+                    }
+                    *(uint4*)(pb + 4 * chunk + ph * 64 + 16 * cg) = z;
+                    *(uint4*)(pb + 4 * chunk + pl * 64 + 16 * cg) = z;
+                    if (cg == 0) ws.q_scale[((size_t)b * s.G + p / R) * R + ph] = 1.f;
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------- merge and W_UV
+// out[v, h, :] = W_UV[h] o_lat[v, h, :],
+// o_lat = sum_p 2^(m_p - m) l_p s_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
+// piece's normalised output in units of s_p.  One CTA per (head, 32 queries): W_UV[h] comes by
+// TMA before the wait for the attention kernel; sixteen warps merge two rows each into the B
+// operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), and D [128 x 32] =
+// W_UV[h] . o_lat^T takes both.
+constexpr int kMergeThreads = 512, kMergeN = 32;
+constexpr int kMergeA = 8 * 128 * 128, kMergeB = 8 * kMergeN * 128;
+constexpr int kMergeSmem = kMergeA + 2 * kMergeB + 64 + 1024;
+
+__global__ void __launch_bounds__(kMergeThreads, 1)
+merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws ws, __nv_bfloat16* __restrict__ out,
+             const DevErr err) {
+    extern __shared__ uint8_t merge_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)merge_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sA = smem, *sB = smem + kMergeA;
+    uint64_t* a_full = (uint64_t*)(sB + 2 * kMergeB);
+    uint64_t* d_full = a_full + 1;
+    uint32_t* tmem_slot = (uint32_t*)(d_full + 1);
+    const Shape& s = src.s;
+    const int h = blockIdx.x, n0 = blockIdx.y * kMergeN, NV = s.B * s.q_len;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(a_full, 1);
+        ptx::mbar_init(d_full, 1);
+        ptx::fence_mbar_init();
+        ptx::mbar_expect_tx(a_full, kMergeA);
+#pragma unroll
+        for (int kc = 0; kc < 8; ++kc) ptx::tma_load_2d(sA + kc * 16384, &tm_w, a_full, 64 * kc, h * 128);
+        pdl_trigger();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(tmem_slot, kMergeN);
+        ptx::tmem_relinquish();
+    }
+    pdl_wait();   // the partials come from the attention kernel
+    const long long per = ws.plan[0];
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int r = warp + 16 * k, v = n0 + r;
+        float acc[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+        if (v < NV) {
+            const int b = v / s.q_len, row = (v % s.q_len) * s.H + h, g = row / s.R, rin = row % s.R;
+            const long long item = (long long)b * s.G + g;
+            const int L = src.len(b), nt = tiles_of(src.keys(L, src.last_token(g)));
+            const long long t0 = ws.plan[1 + (s.sib > 1 ? b : item)] + kPieceCost, k0 = t0 / per;
+            const int np = nt > 0 ? (int)((t0 + nt - 1) / per - k0) + 1 : 0;
+            auto slot_row = [&](int p) -> size_t {
+                const long long slot = p == 0 ? item : (long long)s.B * s.G + (k0 + p) * s.sib + (s.sib > 1 ? g : 0);
+                return (size_t)slot * s.R + rin;
+            };
+            float M = -INFINITY;
+            for (int p = lane; p < np; p += 32) {
+                const float4 ml = ws.part_ml[slot_row(p)];
+                if (ml.y != 0.f) M = fmaxf(M, ml.x);   // a piece without a key of this row has no reference
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            float sum = 0.f;
+            for (int p0 = 0; p0 < np; p0 += 32) {
+                float w = 0.f;
+                if (p0 + lane < np) {
+                    const float4 ml = ws.part_ml[slot_row(p0 + lane)];
+                    const float x = ml.y != 0.f ? exp2f(ml.x - M) * ml.y : 0.f;
+                    sum += x;
+                    w = x * ml.z;
+                }
+                const int n = min(32, np - p0);
+                for (int q0 = 0; q0 < n; q0 += 4) {   // four pieces' rows in flight
+                    uint4 x[4][2];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4* from = (const uint4*)(ws.part_o + slot_row(p0 + min(q0 + q, n - 1)) * kDc + 16 * lane);
+                        x[q][0] = from[0];
+                        x[q][1] = from[1];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float wq = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
+                        if (q0 + q < n && wq != 0.f) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint32_t word = i < 4 ? (&x[q][0].x)[i] : (&x[q][1].x)[i - 4];
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word));
+                                acc[2 * i] = fmaf(wq, f.x, acc[2 * i]);
+                                acc[2 * i + 1] = fmaf(wq, f.y, acc[2 * i + 1]);
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] *= inv;
+        }
+        // columns 16 lane .. +15 of row r: chunk lane / 4, 16-byte units 2 (lane % 4) and + 1
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            hi[i] = ptx::pack_bf16(acc[2 * i], acc[2 * i + 1]);
+            lo[i] = ptx::pack_bf16(acc[2 * i] - __uint_as_float(hi[i] << 16),
+                                   acc[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
+        }
+        uint8_t* at = sB + (lane >> 2) * (kMergeN * 128) + r * 128;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int u = ((2 * (lane & 3) + q) ^ (r & 7)) << 4;
+            *(uint4*)(at + u) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+            *(uint4*)(at + kMergeB + u) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+        }
+    }
+    ptx::fence_proxy_async_smem();   // read by the tensor cores
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 32) {
+        if (!ptx::mbar_wait(a_full, 0, nullptr)) {
+            latch(err, kErrTimeout, 9400000 + h);
+        } else {
+            ptx::tc_fence_after();
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, kMergeN, 0, 0);
+#pragma unroll
+            for (int term = 1; term >= 0; --term)
+#pragma unroll
+                for (int kc = 0; kc < 8; ++kc)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem, ptx::desc_kmajor_sw128(ptx::smem_u32(sA + kc * 16384) + 32 * k),
+                                    ptx::desc_kmajor_sw128(ptx::smem_u32(sB + term * kMergeB + kc * kMergeN * 128) + 32 * k),
+                                    idesc, term == 0 || (kc | k) != 0);
+        }
+        ptx::mma_commit(d_full);
+    }
+    __syncwarp();
+    if (warp < 4) {
+        const bool done = __all_sync(0xffffffffu, ptx::mbar_wait(d_full, 0, nullptr));
+        if (!done && lane == 0) latch(err, kErrTimeout, 9500000 + h);
+        ptx::tc_fence_after();
+        // D (lane = output column, column = query) -> rows of 128 in the A buffer, then whole
+        // 256-byte rows out[v, h, :]
+        __nv_bfloat16* stage = (__nv_bfloat16*)sA;
+        uint32_t r[32];
+        ptx::tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) stage[j * 128 + warp * 32 + lane] = __float2bfloat16_rn(__uint_as_float(r[j]));
+        ptx::named_barrier_sync(1, 128);
+        for (int i = threadIdx.x; i < kMergeN * 16; i += 128) {
+            const int v = n0 + (i >> 4);
+            if (v < NV) ((uint4*)(out + ((size_t)v * s.H + h) * 128))[i & 15] = ((const uint4*)sA)[i];
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) ptx::tmem_dealloc(tmem, kMergeN);
+}
+
+template <typename K>
+cudaError_t set_smem(K kernel, int bytes) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    return e;
+}
+
+template <int R>
+cudaError_t launch_attn(const CUtensorMap& ml, const CUtensorMap& mr, const Src& src, const Problem& p, const Ws& ws,
+                        DevErr err, cudaStream_t st) {
+    cudaError_t e = set_smem(attn_kernel<R>, Cfg<R>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_kernel<R>, dim3(src.s.ctas), dim3(kThreads), Cfg<R>::kSmem, st, ml, mr, src, p.block_table,
+                      p.scales, p.num_pages, p.scale * 1.4426950408889634f, ws, err);
 }
 
 }  // namespace
 
-cudaError_t decode_split(const Problem& p, const float* q_lat, const __nv_bfloat16* q_rope, int ns, float* part_o,
-                         float* part_ml, DevErr err, cudaStream_t s) {
-    constexpr int smem = (kGroup * (kRow + 1) + kWarps * kRow) * 4;
-    cudaError_t e = cudaFuncSetAttribute(decode_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    decode_split_kernel<<<dim3(p.B * p.q_len, ns, (p.H + kWarps - 1) / kWarps), 32 * kWarps, smem, s>>>(
-        p, q_lat, q_rope, ns, part_o, part_ml, err);
-    return cudaGetLastError();
+Shape make_shape(int B, int q_len, int H, int num_sms) {
+    const int rows = q_len * H;
+    Shape s{B, q_len, H, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 1, 1, num_sms};
+    s.G = (rows + s.R - 1) / s.R;
+    s.sib = s.G <= kMaxSib && s.G <= num_sms ? s.G : 1;
+    return s;
 }
+
+Ws carve(char* base, const Shape& s) {
+    const size_t items = (size_t)s.B * s.G, slots = items + s.ctas;
+    Ws w{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) -> char* {
+        char* p = base ? base + off : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    w.q_img = (uint8_t*)take(items * 2 * s.R * kRow);
+    w.q_scale = (float*)take(items * s.R * 4);
+    w.part_o = (__half*)take(slots * s.R * kDc * 2);
+    w.part_ml = (float4*)take(slots * s.R * 16);
+    w.plan = (long long*)take((items + 1) * 8);
+    w.bytes = off;
+    return w;
+}
+
+cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, cudaStream_t st) {
+    const Src src{p.seq_lens, p.max_blocks, s};
+    const uint64_t NV = (uint64_t)s.B * s.q_len, H = s.H;
+    cudaError_t e;
+    CUtensorMap mq, mk, ml, mr, mv;
+    {
+        ProfScope ps(st, "q8_absorb");
+        const uint64_t dq[3] = {128, NV, H}, sq[2] = {H * 256, 256};
+        const uint32_t bq[3] = {64, 128, 1};
+        const uint64_t dw[2] = {128, H * kDc}, sw[1] = {256};
+        const uint32_t bw[2] = {64, 256};
+        if (!make_tmap_bf16(&mq, p.q_nope, 3, dq, sq, bq) || !make_tmap_bf16(&mk, p.W_UKT, 2, dw, sw, bw))
+            return cudaErrorInvalidValue;
+        if ((e = set_smem(absorb_kernel, kAbsorbSmem)) != cudaSuccess) return e;
+        e = launch_pdl(absorb_kernel, dim3(s.H, (unsigned)((NV + 127) / 128)), dim3(kAbsorbThreads), kAbsorbSmem, st, mq,
+                       mk, p.q_rope, s, ws, err);
+        if (e != cudaSuccess) return e;
+    }
+    {
+        ProfScope ps(st, "q8_attention");
+        const uint64_t dc[2] = {kRow, (uint64_t)p.num_pages * kPageRows}, sc[1] = {kRow};
+        const uint32_t bl[2] = {128, kPageRows}, br[2] = {kDr, kPageRows};
+        if (!make_tmap(&ml, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.codes, 2, dc, sc, bl, 128) ||
+            !make_tmap(&mr, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.codes, 2, dc, sc, br, 64))
+            return cudaErrorInvalidValue;
+        e = s.R == 16   ? launch_attn<16>(ml, mr, src, p, ws, err, st)
+            : s.R == 32 ? launch_attn<32>(ml, mr, src, p, ws, err, st)
+                        : launch_attn<64>(ml, mr, src, p, ws, err, st);
+        if (e != cudaSuccess) return e;
+    }
+    ProfScope ps(st, "q8_merge_w_uv");
+    const uint64_t dv[2] = {kDc, H * 128}, sv[1] = {kDc * 2};
+    const uint32_t bv[2] = {64, 128};
+    if (!make_tmap_bf16(&mv, p.W_UV, 2, dv, sv, bv)) return cudaErrorInvalidValue;
+    if ((e = set_smem(merge_kernel, kMergeSmem)) != cudaSuccess) return e;
+    return launch_pdl(merge_kernel, dim3(s.H, (unsigned)((NV + kMergeN - 1) / kMergeN)), dim3(kMergeThreads), kMergeSmem,
+                      st, mv, src, ws, p.out, err);
+}
+
+cudaError_t set_wait_limit_decode_q8(uint32_t polls) { return ptx::set_wait_limit_of_this_file(polls); }
 
 }  // namespace q8
 }  // namespace mla

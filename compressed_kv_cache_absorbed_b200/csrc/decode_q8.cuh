@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -11,21 +12,45 @@
 namespace mla {
 namespace q8 {
 
-struct Problem {
-    int H, B, q_len;            // heads (<= 128), sequences, new tokens per sequence
-    const uint8_t* codes;       // [num_pages, 64, 576]
-    const float* scales;        // [num_pages]
-    long long num_pages;
-    const int32_t* block_table; // [B, max_blocks]
-    const int32_t* seq_lens;    // [B]
-    int max_blocks;
-    float scale;                // softmax scale
+// How the rows (new token t, head h) of a sequence, r = t H + h, are cut into groups of R
+// rows, and how many CTAs walk one sequence's tiles side by side.
+struct Shape {
+    int B, q_len, H;
+    int R;        // rows per group: 16, 32 or 64
+    int G;        // groups per sequence
+    int sib;      // > 1: the G groups of a sequence are walked by G neighbouring CTAs; 1: one after another
+    int ctas;     // CTAs of the attention kernel
 };
 
-// Split-KV attention on CUDA cores: part_o [ns, B q_len, H, 512] unnormalised, part_ml
-// [ns, B q_len, H, 2] (running max of the scaled scores, sum), fp32.
-cudaError_t decode_split(const Problem& p, const float* q_lat, const __nv_bfloat16* q_rope, int ns, float* part_o,
-                         float* part_ml, DevErr err, cudaStream_t s);
+Shape make_shape(int B, int q_len, int H, int num_sms);
+
+struct Ws {
+    uint8_t* q_img;     // [B G][2 R rows x 576]: the queries as 8-bit operands
+    float* q_scale;     // [B G][R]
+    __half* part_o;     // [slots][R][512] normalised partial outputs
+    float4* part_ml;    // [slots][R] (reference, sum, scale of the output, -)
+    long long* plan;    // [1 + vseqs]: cost units per range, cost position of each virtual sequence
+    size_t bytes;
+};
+
+Ws carve(char* base, const Shape& s);
+
+struct Problem {
+    const __nv_bfloat16 *q_nope, *q_rope;   // [B q_len, H, 128], [B q_len, H, 64]
+    const __nv_bfloat16 *W_UKT, *W_UV;      // [H, 512, 128], [H, 128, 512]
+    const uint8_t* codes;                   // [num_pages, 64, 576]
+    const float* scales;                    // [num_pages]
+    long long num_pages;
+    const int32_t* block_table;             // [B, max_blocks]
+    const int32_t* seq_lens;                // [B]
+    int max_blocks;
+    float scale;                            // softmax scale
+    __nv_bfloat16* out;                     // [B q_len, H, 128]
+};
+
+cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, cudaStream_t st);
+
+cudaError_t set_wait_limit_decode_q8(uint32_t polls);
 
 }  // namespace q8
 }  // namespace mla
