@@ -41,7 +41,7 @@ constexpr int kDc = 512, kDr = 64, kRow = 576;
 constexpr int kT = 128;                       // tokens per tile
 constexpr int kChunkBytes = kT * 128;         // 128 latent columns of a tile (128-byte swizzle)
 constexpr int kRopeBytes = kT * kDr;          // the rotary columns of a tile (64-byte swizzle)
-constexpr int kThreads = 320;                 // TMA warp, MMA warp, 8 softmax warps
+constexpr int kRoleThreads = 128;             // TMA warp, score issuer, O issuer, a warp without a role
 constexpr int kPieceCost = 1;                 // cost units of a piece's query load and epilogue, in tiles
 constexpr int kMaxSib = 8;
 constexpr float kTopLog2 = 8.5f;              // p <= 2^8.5
@@ -50,11 +50,14 @@ constexpr float kFarLog2 = 64.f;              // how far below its highest value
 
 // Shared memory: NC chunk slots, NR slots that hold a tile's rotary columns and then its P
 // (hi and, for R <= 32, lo), P's lo term (R = 64), the group's queries.
+// Softmax warps: four (one per 32 tokens) for each of CG groups of HC rows; 16 rows a thread
+// keep its scores, sums and references in registers beside four warps per scheduler.
 template <int R> struct Cfg {
-    static constexpr int HC = R / 2;                     // rows per softmax thread
+    static constexpr int HC = R == 16 ? 8 : 16, CG = R / HC;
+    static constexpr int kSoft = 128 * CG, kThreads = kRoleThreads + kSoft;
     static constexpr bool kTwoPass = R == 64;            // P hi and lo as two products (one accumulator)
     static constexpr int NP = kTwoPass ? R : 2 * R;      // N of an O product
-    static constexpr int NC = R == 64 ? 8 : R == 32 ? 10 : 11;
+    static constexpr int NC = R == 64 ? 8 : 10;
     static constexpr int NR = 2;
     static constexpr int kLoBytes = kTwoPass ? kRopeBytes : 0;
     static constexpr int kQBytes = 2 * R * kRow;
@@ -66,26 +69,44 @@ template <int R> struct Cfg {
     static_assert(kSmem <= 232448, "shared memory over the 227 KB limit");
 };
 
-// tcgen05.mma kind::f8f6f4, both operands in shared memory
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// tcgen05.mma kind::f8f6f4, both operands in shared memory, issued by the lane whose `lead` is
+// set.  The whole warp runs the issue loops with warp-uniform values, so that descriptors stay
+// in uniform registers: from one thread's branch, each product took ~105 cycles to issue, twice
+// what the smallest ones take to run.  Only the low words of the descriptors (address,
+// leading offset) vary.
+__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                       uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
+// A value that is the same in all lanes, as one the compiler knows to be so (loops around the
+// products run on it)
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x); }
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+// Descriptor words: low = address and leading offset (both / 16), high = stride offset / 16,
+// version 1, swizzle (2: 128 bytes, 4: 64 bytes)
+__device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 // E4M3 x E4M3 -> fp32
 constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major, int b_mn_major) {
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
-// MN-major operand in 64-byte-swizzled atoms: 64 one-byte MN elements per row, 8 K-rows per
-// 512-byte atom (N <= 64: one atom wide)
-__device__ __forceinline__ uint64_t desc_mnmajor_sw64(uint32_t saddr) { return ptx::smem_desc(saddr, 512, 512, 4); }
-
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { ptx::tmem_ld32(taddr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -98,7 +119,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { ptx::tmem_st32(taddr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) { ptx::tmem_st16(taddr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -109,6 +129,12 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) 
 __device__ __forceinline__ float ex2(float x) {   // flushes results below 2^-126
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// largest value of a warp's lanes (NaN does not count)
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
 // two values -> two E4M3 codes, `lo` in the low byte (nearest even, saturating, NaN kept)
@@ -160,38 +186,51 @@ struct Src {
 __device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kT - 1) / kT : 0; }
 __device__ __forceinline__ long long cost_of(int n) { return n > 0 ? n + kPieceCost : 0; }
 
-// tiles [j0, j1) of group g of sequence b
+// tiles [j0, j1) of group g of sequence b (j0 = j1: no more pieces)
 struct Seg {
-    int b, item, g, j0, j1, len, kmin, kmax, slot;
+    int b, item, g, j0, j1, len, kmin, kmax, slot, pad[3];
 };
+static_assert(sizeof(Seg) % 16 == 0, "alignment of what lies behind");
+// Walks the pieces of this CTA's range.  Positions are counted from the range's start.
 struct SegIter {
-    Src src;
-    int nv, sib_idx, cta;
-    long long lo, hi, cs;
+    const Src& src;
+    int span;   // cost units of the range
+    int cs;     // where virtual sequence i's cost starts (not above 0 at first)
     int i;
     __device__ bool next(Seg& s) {
-        while (i < nv && cs < hi) {
+        const int nv = src.vseqs();
+        while (i < nv && cs < span) {
             const int ii = i++;
             const int n = tiles_of(src.vlen(ii));
-            const long long f = cs + kPieceCost;
-            cs += cost_of(n);
+            const int f = cs + kPieceCost;
+            cs += (int)cost_of(n);
             if (n == 0) continue;
             s.b = src.s.sib > 1 ? ii : ii / src.s.G;
-            s.g = src.s.sib > 1 ? sib_idx : ii % src.s.G;
+            s.g = src.s.sib > 1 ? (int)blockIdx.x % src.s.sib : ii % src.s.G;
             s.item = s.b * src.s.G + s.g;
             s.len = src.len(s.b);
             s.kmin = src.keys(s.len, src.first_token(s.g));
             s.kmax = src.keys(s.len, src.last_token(s.g));
-            s.j0 = lo > f ? (int)(lo - f) : 0;
-            s.j1 = (int)min(hi - f, (long long)tiles_of(s.kmax));
+            s.j0 = max(-f, 0);
+            s.j1 = min(span - f, tiles_of(s.kmax));
             if (s.j0 < s.j1) {
-                s.slot = s.j0 == 0 ? s.item : src.s.B * src.s.G + cta;
+                s.slot = s.j0 == 0 ? s.item : src.s.B * src.s.G + (int)blockIdx.x;
                 return true;
             }
         }
         return false;
     }
 };
+
+// A bounded wait of a whole warp, in few instructions (the kernel has some thirty of them)
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
+    uint32_t left = ptx::g_wait_limit;
+#pragma unroll 1
+    do {
+        if (__all_sync(0xffffffffu, ptx::mbar_try(bar, parity))) return true;
+    } while (--left != 0 && !(__any_sync(0xffffffffu, *abort_flag != 0)));
+    return false;
+}
 
 __device__ __forceinline__ void fail(DevErr err, volatile int* abort_flag, int where) {
     latch(err, kErrTimeout, (long long)where * 1000000 + blockIdx.x);
@@ -200,12 +239,12 @@ __device__ __forceinline__ void fail(DevErr err, volatile int* abort_flag, int w
 
 // ------------------------------------------------------------------ attention
 template <int R>
-__global__ void __launch_bounds__(kThreads, 1)
-attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope, const Src src,
+__global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
+attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ Src src,
             const int32_t* __restrict__ block_table, const float* __restrict__ scales, long long num_pages,
-            float scale_log2, const Ws ws, const DevErr err) {
+            float scale_log2, const __grid_constant__ Ws ws, const DevErr err) {
     using C = Cfg<R>;
-    constexpr int HC = C::HC, NC = C::NC, NR = C::NR;
+    constexpr int HC = C::HC, CG = C::CG, NC = C::NC, NR = C::NR, kThreads = C::kThreads;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (ptx::smem_u32(smem) & 1023) {   // uniform: leave before any barrier
         if (threadIdx.x == 0) latch(err, kErrTimeout, 9000000);
@@ -215,22 +254,25 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     uint8_t* ropes = chunks + NC * kChunkBytes;
     uint8_t* plo = ropes + NR * kRopeBytes;
     uint8_t* qimg = plo + C::kLoBytes;
-    float* qs = (float*)(qimg + C::kQBytes);            // [2][R] row scales of this piece's and the next's queries
-    float4* red = (float4*)(qs + 2 * 64);               // [2][32] per row, one value per token quarter
-    float* tops = (float*)(red + 64);                   // [2][4][32] each warp's highest references; sums at a piece's end
-    uint64_t* bars = (uint64_t*)(tops + 256);
-    uint64_t *chunk_full = bars, *chunk_empty = bars + 11, *rope_full = bars + 22, *rope_empty = bars + 24;
-    uint64_t *q_full = bars + 26, *s_full = bars + 27, *s_free = bars + 29, *p_ready = bars + 31;
-    uint64_t *lo_free = bars + 33, *o_done = bars + 34, *half_bar = bars + 36, *drain = bars + 38;
-    float* page_scale = (float*)(bars + 40);            // [4 tiles][2 pages]
-    uint32_t* flags = (uint32_t*)(page_scale + 8);      // [2 tiles][2 halves][4]
-    uint32_t* tmem_slot = flags + 16;
+    float* qs = (float*)(qimg + C::kQBytes);            // [R] row scales of the queries
+    float4* red = (float4*)(qs + 64);                   // [CG][16] per row, one value per token quarter
+    float* refs = (float*)(red + 64);                   // [CG][16] each row's reference
+    uint64_t* bars = (uint64_t*)(refs + 64);
+    uint64_t *chunk_full = bars, *chunk_empty = bars + NC, *rope_full = bars + 2 * NC, *rope_empty = rope_full + 2;
+    uint64_t *q_full = rope_full + 4, *s_full = rope_full + 5, *s_free = rope_full + 7, *p_ready = rope_full + 9;
+    uint64_t *o_done = rope_full + 12, *grp_bar = rope_full + 14, *drain = rope_full + 18;
+    uint64_t *seg_full = rope_full + 20, *seg_empty = rope_full + 22;
+    Seg* segs = (Seg*)(rope_full + 24);                 // [2] the pieces of this CTA, from the planning warp
+    uint32_t* flags = (uint32_t*)(segs + 2);            // [2 tiles][CG][4]
+    float* page_scale = (float*)(flags + 32);           // [4 tiles][2 pages]
+    float* out_scale = page_scale + 8;                  // [CG][4] largest page scale a warp saw
+    uint32_t* tmem_slot = (uint32_t*)(out_scale + 16);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-    float* out_scale = (float*)(tmem_slot + 2);         // [2 halves][4] largest page scale a warp saw
-    static_assert(2 * 64 * 4 + 64 * 16 + 256 * 4 + 40 * 8 + 8 * 4 + 16 * 4 + 8 + 8 * 4 <= C::kMisc, "barrier area");
+    static_assert(64 * 4 + 64 * 16 + 64 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
+    static_assert(NC % 2 == 0, "16-byte alignment of the words behind the barriers");
     // the planning's scratch lies where the reductions come later
-    long long* plan_wsum = (long long*)red;             // [10]
-    long long* plan_first = plan_wsum + 10;             // [2]
+    long long* plan_wsum = (long long*)red;             // [kThreads / 32]
+    long long* plan_first = plan_wsum + 32;             // [2]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -244,14 +286,15 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&s_free[i], 256);
-            ptx::mbar_init(&p_ready[i], 256);
-            ptx::mbar_init(&half_bar[i], 4);
+            ptx::mbar_init(&s_free[i], C::kSoft);
+            ptx::mbar_init(&p_ready[i], C::kSoft);
             ptx::mbar_init(&o_done[i], 1);
+            ptx::mbar_init(&seg_full[i], 1);
+            ptx::mbar_init(&seg_empty[i], kThreads / 32 - 1);
         }
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&grp_bar[i], 4);
         ptx::mbar_init(q_full, 1);
-        ptx::mbar_init(lo_free, 1);
-        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(drain, 2);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::tma_prefetch(&tm_lat);
@@ -268,7 +311,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     // lengths, table and cache are final.
     constexpr int kWarps = kThreads / 32;
     const int nv = src.vseqs(), ranges = src.s.ctas / src.s.sib;
-    const int range = (int)blockIdx.x / src.s.sib, sib_idx = (int)blockIdx.x % src.s.sib;
+    const int range = (int)blockIdx.x / src.s.sib;
     long long total = 0;
     {
         long long mine = 0;
@@ -325,22 +368,47 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             __syncthreads();
         }
     }
-    SegIter it{src, nv, sib_idx, (int)blockIdx.x, lo, hi, plan_first[1], (int)plan_first[0]};
-    const uint32_t tmem = *tmem_slot;
+    SegIter it{src, (int)(hi - lo), (int)(plan_first[1] - lo), (int)plan_first[0]};
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
     __syncthreads();   // plan_first is read before red is written
 
+    // The pieces, in order, as every role sees them: warp 3 finds them ahead of time
     Seg sg;
-    if (warp == 0) {
+    uint32_t segs_seen = 0;
+    auto next_piece = [&]() -> bool {
+        const uint32_t k = segs_seen & 1;
+        if (!wait_warp(&seg_full[k], (segs_seen >> 1) & 1, abort_flag)) return false;
+        sg = segs[k];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&seg_empty[k]);
+        ++segs_seen;
+        return uniform(sg.j0 < sg.j1);
+    };
+    if (warp == 3) {
+        bool more = true;
+#pragma unroll 1
+        for (uint32_t n = 0; more; ++n) {
+            more = it.next(sg);
+            if (n >= 2 && !wait_warp(&seg_empty[n & 1], ((n >> 1) - 1) & 1, abort_flag)) break;
+            if (!more) sg.j0 = sg.j1 = 0;
+            if (lane == 0) {
+                segs[n & 1] = sg;
+                ptx::mbar_arrive(&seg_full[n & 1]);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
         // lane l holds the page (and its scale) of block base + l of the sequence
         const uint64_t policy = src.s.G > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
         const long long none = num_pages * kPageRows;   // a box past the last row reads zeros
         uint32_t g = 0, cn = 0;                         // tiles, chunks requested
         bool ok = true;
-        while (ok && !*abort_flag && it.next(sg)) {
+        while (ok && next_piece()) {
             const int blocks = (sg.len + kPageRows - 1) / kPageRows;
             long long row = none;
             float sc = 0.f;
+#pragma unroll 1
             for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
                 const int at = (j - sg.j0) & 15;
                 if (at == 0) {
@@ -390,143 +458,115 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 ptx::mbar_wait(&rope_full[(g - 1 - k) % NR], ((g - 1 - k) / NR) & 1, nullptr);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        // Event-driven: O of the oldest tile whose P is written, else the next score step (one
-        // 128-column chunk, or the rotary columns) whose data has landed.  Scores run at most
-        // two tiles ahead of O.
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_e4m3(128, 2 * R, 0, 0);
-            constexpr uint32_t idesc_o = idesc_e4m3(128, C::NP, 1, 1);
-            const uint32_t chunk0 = ptx::smem_u32(chunks), rope0 = ptx::smem_u32(ropes), lo0 = ptx::smem_u32(plo),
-                           q0 = ptx::smem_u32(qimg);
-            SegIter its = it;
-            Seg ss;
-            bool s_have = !*abort_flag && its.next(ss), o_have = !*abort_flag && it.next(sg);
-            int s_j = s_have ? ss.j0 : 0, o_j = o_have ? sg.j0 : 0, s_c = 0;
-            uint32_t s_g = 0, o_g = 0, piece = 0, idle = 0;
-            bool ok = true;
-            while (o_have) {
-                if (o_g < s_g && ptx::mbar_test(&p_ready[o_g & 1], (o_g >> 1) & 1)) {
+        // ---------------------------------------------- queries and score products
+        const uint32_t lead = lane == 0;
+        constexpr uint32_t idesc = idesc_e4m3(128, 2 * R, 0, 0);
+        constexpr uint32_t h128 = desc_hi(1024, 2), h64 = desc_hi(512, 4);
+        const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), 16), rope0 = desc_lo(ptx::smem_u32(ropes), 16),
+                       q0 = desc_lo(ptx::smem_u32(qimg), 16);
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, abort_flag); };
+        pdl_wait();   // the queries come from the previous kernel of this call
+        uint32_t g = 0, piece = 0, slot = 0, use = 0;   // tile, piece, chunk slot and how often the slots were gone through
+        bool ok = true;
+        while (ok && next_piece()) {
+            // Every softmax thread has read the last scores: their products are done with the
+            // queries, and it is done with the row scales.
+            if (g > 0 && !wait(&s_free[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
+            if (lead) {
+                ptx::mbar_expect_tx(q_full, C::kQBytes + R * 4);
+                const uint8_t* from = ws.q_img + (size_t)sg.item * C::kQBytes;
+                for (int o = 0; o < C::kQBytes; o += C::kQBytes / 4)
+                    ptx::bulk_load(qimg + o, from + o, C::kQBytes / 4, q_full);
+                ptx::bulk_load(qs, ws.q_scale + (size_t)sg.item * R, R * 4, q_full);
+            }
+            __syncwarp();
+            // in flight after an abort: waited for without a look at the flag
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(q_full, piece & 1, nullptr))) { ok = false; break; }
+            ++piece;
+#pragma unroll 1
+            for (int left = uniform(sg.j1 - sg.j0); left > 0; --left, ++g) {
+                if (g >= 2 && !wait(&s_free[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
+                const uint32_t d = tmem + (g & 1) * (2 * R);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (!wait(&chunk_full[slot], use & 1)) { ok = false; break; }
                     ptx::tc_fence_after();
-                    const uint32_t acc0 = o_j != sg.j0;
-                    const uint32_t p_hi = rope0 + (o_g % NR) * kRopeBytes;
-                    if (C::kTwoPass) {   // the lo terms first: their buffer is free for the next tile sooner
+                    const uint32_t a = chunk0 + slot * (kChunkBytes >> 4), b = q0 + c * (2 * R * 128 >> 4);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t a = chunk0 + ((4 * o_g + c) % NC) * kChunkBytes;
+                    for (int k = 0; k < 4; ++k) mma_f8(lead, d, a + 2 * k, h128, b + 2 * k, h128, idesc, (c | k) != 0);
+                    if (++slot == NC) slot = 0, ++use;
+                }
+                if (!ok || !wait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }
+                ptx::tc_fence_after();
+                const uint32_t a = rope0 + (g % NR) * (kRopeBytes >> 4), b = q0 + 4 * (2 * R * 128 >> 4);
 #pragma unroll
-                            for (int k = 0; k < kT / 32; ++k)
-                                mma_f8(tmem + C::kColO + c * C::NP, ptx::desc_mnmajor_sw128(a + 4096 * k, kChunkBytes),
-                                       desc_mnmajor_sw64(lo0 + 2048 * k), idesc_o, acc0 | (k > 0));
-                        }
-                        ptx::mma_commit(lo_free);
-                    }
+                for (int k = 0; k < 2; ++k) mma_f8(lead, d, a + 2 * k, h64, b + 2 * k, h64, idesc, 1);
+                commit(lead, &s_full[g & 1]);
+            }
+        }
+        if (!ok && lead) fail(err, abort_flag, 12);
+        commit(lead, drain);
+        if (!ptx::mbar_wait(drain, 0, nullptr) && lead) fail(err, abort_flag, 14);
+    } else if (warp == 2) {
+        // ---------------------------------------------------------- O products
+        const uint32_t lead = lane == 0;
+        constexpr uint32_t idesc = idesc_e4m3(128, C::NP, 1, 1);
+        constexpr uint32_t h128 = desc_hi(1024, 2), h64 = desc_hi(512, 4);
+        const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), kChunkBytes), rope0 = desc_lo(ptx::smem_u32(ropes), 512),
+                       lo0 = desc_lo(ptx::smem_u32(plo), 512);
+        uint32_t g = 0, slot0 = 0;
+        bool ok = true;
+        while (ok && next_piece()) {
+            uint32_t acc0 = 0;
+#pragma unroll 1
+            for (int left = uniform(sg.j1 - sg.j0); left > 0; --left, ++g) {
+                if (!wait_warp(&p_ready[g & 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+                ptx::tc_fence_after();
+                const uint32_t p = rope0 + (g % NR) * (kRopeBytes >> 4);
+                // chunk by chunk, so that the first slots are free for the next loads early
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t slot = (4 * o_g + c) % NC, a = chunk0 + slot * kChunkBytes;
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t a = chunk0 + slot0 * (kChunkBytes >> 4), d = tmem + C::kColO + c * C::NP;
+#pragma unroll
+                    for (int k = 0; k < kT / 32; ++k)
+                        mma_f8(lead, d, a + 256 * k, h128, p + 128 * k, h64, idesc, acc0 | (k > 0));
+                    if (C::kTwoPass) {
 #pragma unroll
                         for (int k = 0; k < kT / 32; ++k)
-                            mma_f8(tmem + C::kColO + c * C::NP, ptx::desc_mnmajor_sw128(a + 4096 * k, kChunkBytes),
-                                   desc_mnmajor_sw64(p_hi + 2048 * k), idesc_o, C::kTwoPass || acc0 | (k > 0));
-                        ptx::mma_commit(&chunk_empty[slot]);
+                            mma_f8(lead, d, a + 256 * k, h128, lo0 + 128 * k, h64, idesc, 1);
                     }
-                    ptx::mma_commit(&o_done[o_g & 1]);
-                    ptx::mma_commit(&rope_empty[o_g % NR]);
-                    ++o_g;
-                    if (++o_j == sg.j1) {
-                        o_have = it.next(sg);
-                        o_j = o_have ? sg.j0 : 0;
-                    }
-                    idle = 0;
-                    continue;
+                    commit(lead, &chunk_empty[slot0]);
+                    if (++slot0 == NC) slot0 = 0;
                 }
-                if (s_have && s_g < o_g + 2) {
-                    bool ready;
-                    if (s_c < 4) {
-                        const uint32_t cn = 4 * s_g + s_c;
-                        ready = ptx::mbar_test(&chunk_full[cn % NC], (cn / NC) & 1);
-                        if (s_c == 0)
-                            ready = ready && (s_g < 2 || ptx::mbar_test(&s_free[s_g & 1], ((s_g >> 1) - 1) & 1)) &&
-                                    (s_j != ss.j0 || ptx::mbar_test(q_full, piece & 1));
-                    } else {
-                        ready = ptx::mbar_test(&rope_full[s_g % NR], (s_g / NR) & 1);
-                    }
-                    if (ready) {
-                        ptx::tc_fence_after();
-                        const uint32_t d = tmem + (s_g & 1) * (2 * R);
-                        if (s_c < 4) {
-                            const uint32_t a = chunk0 + ((4 * s_g + s_c) % NC) * kChunkBytes, b = q0 + s_c * (2 * R * 128);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f8(d, ptx::desc_kmajor_sw128(a + 32 * k), ptx::desc_kmajor_sw128(b + 32 * k), idesc_s,
-                                       (s_c | k) != 0);
-                            ++s_c;
-                        } else {
-                            const uint32_t a = rope0 + (s_g % NR) * kRopeBytes, b = q0 + 4 * (2 * R * 128);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                mma_f8(d, ptx::desc_kmajor_sw64(a + 32 * k), ptx::desc_kmajor_sw64(b + 32 * k), idesc_s, 1);
-                            ptx::mma_commit(&s_full[s_g & 1]);
-                            s_c = 0;
-                            ++s_g;
-                            if (++s_j == ss.j1) {
-                                s_have = its.next(ss);
-                                s_j = s_have ? ss.j0 : 0;
-                                ++piece;
-                            }
-                        }
-                        idle = 0;
-                        continue;
-                    }
-                }
-                // polls do not block here: 16 of them count as one of the other waits'
-                if (++idle > (ptx::g_wait_limit << 4) || *abort_flag) {
-                    ok = false;
-                    break;
-                }
+                commit(lead, &o_done[g & 1]);
+                commit(lead, &rope_empty[g % NR]);
+                acc0 = 1;
             }
-            if (!ok) fail(err, abort_flag, 12);
-            ptx::mma_commit(drain);
-            if (!ptx::mbar_wait(drain, 0, nullptr)) fail(err, abort_flag, 14);
         }
-    } else {
+        if (!ok && lead) fail(err, abort_flag, 16);
+        commit(lead, drain);
+        if (!ptx::mbar_wait(drain, 0, nullptr) && lead) fail(err, abort_flag, 17);
+    } else if (warp >= kRoleThreads / 32) {
         // ------------------------------------------------- softmax and epilogue
-        const int quad = warp & 3, half = warp >= 6 ? 1 : 0;
+        const int quad = warp & 3, grp = (warp - kRoleThreads / 32) >> 2;
         const int tok = 32 * quad + lane;                       // token of the tile = TMEM lane
-        const int c0 = half * HC;                               // first row of this thread
+        const int c0 = grp * HC;                                // first row of this thread
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * quad) << 16);
-        const bool loader = warp == 2 && lane == 0;             // requests the queries
         bool ok = true;
-        auto uwait = [&](uint64_t* bar, uint32_t parity) {      // warp-uniform result
-            return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag));
-        };
+        auto uwait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, abort_flag); };
         uint32_t meets = 0;
-        auto meet = [&]() {   // the four warps that share this half's rows
+        auto meet = [&]() {   // the four warps that share these rows
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&half_bar[half]);
-            if (!uwait(&half_bar[half], meets & 1)) ok = false;
+            if (lane == 0) ptx::mbar_arrive(&grp_bar[grp]);
+            if (!uwait(&grp_bar[grp], meets & 1)) ok = false;
             ++meets;
         };
-        auto load_q = [&](const Seg& s, uint32_t piece) {
-            ptx::mbar_expect_tx(q_full, C::kQBytes + R * 4);
-            const uint8_t* from = ws.q_img + (size_t)s.item * C::kQBytes;
-            for (int o = 0; o < C::kQBytes; o += C::kQBytes / 4)
-                ptx::bulk_load(qimg + o, from + o, C::kQBytes / 4, q_full);
-            ptx::bulk_load(qs + (piece & 1) * 64, ws.q_scale + (size_t)s.item * R, R * 4, q_full);
-        };
-        pdl_wait();   // the queries come from the previous kernel of this call
-        Seg nxt;
-        bool have = it.next(sg);
-        uint32_t piece = 0, g = 0, q_loads = 0;
-        if (loader && have) {
-            load_q(sg, 0);
-            ++q_loads;
-        }
-        float M[HC], l[HC];
-        while (have && ok) {
-            const bool more = it.next(nxt);
+        uint32_t piece = 0, g = 0;
+        float l[HC];               // this thread's share of each row's sum
+        float m_row = 0.f, m_top = 0.f;   // lane i: reference of row c0 + i, and the highest it has had
+        while (ok && next_piece()) {
             float s_ref = 1.f, s_top = 0.f;
-            const float* qsp = qs + (piece & 1) * 64 + c0;
+#pragma unroll 1
             for (int j = sg.j0; j < sg.j1; ++j, ++g) {
                 const bool first = j == sg.j0;
                 if (first && !uwait(q_full, piece & 1)) { ok = false; break; }   // row scales
@@ -543,39 +583,35 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     tmem_ld(lane_addr + (g & 1) * (2 * R) + R + c0, b);
                     ptx::tmem_wait_ld();
                     ptx::tc_fence_before();
-                    ptx::mbar_arrive(&s_free[g & 1]);
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) arg[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
-                }
-                if (loader && j + 1 == sg.j1 && more) {
-                    // The piece's last scores are done with its queries.  Every warp has read
-                    // these scores, so it has seen q_full of this piece and is done with the
-                    // row scales of the one before.
-                    if (!ptx::mbar_wait(&s_free[g & 1], (g >> 1) & 1, abort_flag)) {
-                        fail(err, abort_flag, 15);
-                    } else {
-                        load_q(nxt, piece + 1);
-                        ++q_loads;
+                    for (int i = 0; i < HC; i += 4) {
+                        const float4 f = *(const float4*)(qs + c0 + i);
+                        arg[i] = (__uint_as_float(a[i]) + __uint_as_float(b[i])) * f.x;
+                        arg[i + 1] = (__uint_as_float(a[i + 1]) + __uint_as_float(b[i + 1])) * f.y;
+                        arg[i + 2] = (__uint_as_float(a[i + 2]) + __uint_as_float(b[i + 2])) * f.z;
+                        arg[i + 3] = (__uint_as_float(a[i + 3]) + __uint_as_float(b[i + 3])) * f.w;
                     }
+                    ptx::mbar_arrive(&s_free[g & 1]);   // also done with the row scales
                 }
                 float s = page_scale[2 * (g & 3) + (quad >> 1)];
                 if (first) {
                     const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
                     s_ref = sa != 0.f ? sa : sb != 0.f ? sb : 1.f;
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) M[i] = 0.f, l[i] = 0.f;
+                    for (int i = 0; i < HC; ++i) l[i] = 0.f;
+                    m_row = 0.f;
                 }
                 s_top = fmaxf(s_top, s);
                 if (s == 0.f) s = s_ref;   // no page: zero rows
                 const bool same = s == s_ref;
                 const float kt = scale_log2 * s, shift = same ? 0.f : log2f(s) - log2f(s_ref), back = same ? 1.f : s_ref / s;
 #pragma unroll
-                for (int i = 0; i < HC; i += 4) {
-                    const float4 f = *(const float4*)(qsp + i);
-                    arg[i] = fmaf(arg[i], f.x * kt, shift - M[i]);
-                    arg[i + 1] = fmaf(arg[i + 1], f.y * kt, shift - M[i + 1]);
-                    arg[i + 2] = fmaf(arg[i + 2], f.z * kt, shift - M[i + 2]);
-                    arg[i + 3] = fmaf(arg[i + 3], f.w * kt, shift - M[i + 3]);
+                for (int i = 0; i < HC; i += 4) {   // the first tile's arguments are set when its reference is
+                    const float4 m = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *(const float4*)(refs + grp * 16 + i);
+                    arg[i] = fmaf(arg[i], kt, shift - m.x);
+                    arg[i + 1] = fmaf(arg[i + 1], kt, shift - m.y);
+                    arg[i + 2] = fmaf(arg[i + 2], kt, shift - m.z);
+                    arg[i + 3] = fmaf(arg[i + 3], kt, shift - m.w);
                 }
                 const bool edge = (j + 1) * kT > sg.kmin;   // some row does not see the whole tile
                 if (edge) {
@@ -586,9 +622,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                             for (int i = 0; i < HC; ++i) arg[i] = -INFINITY;
                         }
                     } else {
+                        const int row = sg.g * R + c0;
+                        int t = row / src.s.H, h = row - t * src.s.H;   // of the thread's first row
+                        int keys = src.keys(sg.len, t);
 #pragma unroll
-                        for (int i = 0; i < HC; ++i)
-                            if (at >= src.keys(sg.len, (sg.g * R + c0 + i) / src.s.H)) arg[i] = -INFINITY;
+                        for (int i = 0; i < HC; ++i) {
+                            if (at >= keys) arg[i] = -INFINITY;
+                            if (++h == src.s.H) h = 0, ++keys;
+                        }
                     }
                 }
                 // Does every row keep its reference?  Sign bits of the arguments, anded over the
@@ -604,63 +645,55 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     }
                     low = __reduce_and_sync(0xffffffffu, low);
                     if (__any_sync(0xffffffffu, top > kTopLog2)) low = 0xffffffffu;
-                    if (lane == 0) flags[(g & 1) * 8 + half * 4 + quad] = low;
+                    if (lane == 0) flags[((g & 1) * CG + grp) * 4 + quad] = low;
                 }
                 meet();
                 if (!ok) break;
-                const uint4 fl = *(const uint4*)(flags + (g & 1) * 8 + half * 4);
+                const uint4 fl = *(const uint4*)(flags + ((g & 1) * CG + grp) * 4);
                 const bool over = fl.x == 0xffffffffu || fl.y == 0xffffffffu || fl.z == 0xffffffffu || fl.w == 0xffffffffu;
                 if (first || over || (fl.x & fl.y & fl.z & fl.w) != 0) {
-                    float keep = -INFINITY;   // lane i: this warp's largest z' of row c0 + i
+                    // this warp's largest argument of each row, then the tile's, row i in lane i
+                    float keep = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < HC; ++i) {
-                        float v = arg[i] + M[i];
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                        const float v = warp_max(arg[i]);
                         if (lane == i) keep = v;
                     }
-                    if (lane < HC) ((float*)red)[(half * 32 + lane) * 4 + quad] = keep;
+                    if (lane < HC) ((float*)(red + grp * 16 + lane))[quad] = keep;
                     meet();
                     if (!ok) break;
-                    bool moved = false;
-                    float alpha[HC];
-                    float* my_top = tops + (half * 4 + quad) * 32;
-#pragma unroll
-                    for (int i = 0; i < HC; ++i) {
-                        const float4 v = red[half * 32 + i];
+                    float step = 0.f;   // new reference - old one
+                    if (lane < HC) {
+                        const float4 v = red[grp * 16 + lane];
                         const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                        float m = M[i];
-                        if (mx > -INFINITY && (first || mx - m > kTopLog2 || mx < m)) {
-                            m = mx - kSetLog2;
-                            if (!first) m = fmaxf(m, my_top[i] - kFarLog2);
+                        if (mx > -INFINITY && (first || mx > kTopLog2 || mx < 0.f)) {
+                            step = mx - kSetLog2;
+                            if (!first) step = fmaxf(step, m_top - kFarLog2 - m_row);
                         }
-                        alpha[i] = ex2(M[i] - m);
-                        arg[i] += M[i] - m;
-                        moved = moved || (!first && m != M[i]);
-                        M[i] = m;
+                        m_row += step;
+                        m_top = first ? m_row : fmaxf(m_top, m_row);
+                        refs[grp * 16 + lane] = m_row;   // the four warps write the same
                     }
+                    const float alpha = ex2(-step);
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < HC; ++i)
-                        if (lane == i) my_top[i] = first ? M[i] : fmaxf(my_top[i], M[i]);
-                    __syncwarp();
-                    if (moved) {   // the same for all token lanes
+                    for (int i = 0; i < HC; ++i) arg[i] -= __shfl_sync(0xffffffffu, step, i);
+                    if (!first && __any_sync(0xffffffffu, step != 0.f)) {   // the same in the four warps
                         if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
                         ptx::tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < HC; ++i) l[i] *= alpha[i];
+                        for (int i = 0; i < HC; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll 1
-                            for (int term = 0; term < C::NP / R; ++term) {
-                                uint32_t r[HC];
-                                const uint32_t ad = lane_addr + C::kColO + c * C::NP + term * R + c0;
-                                tmem_ld(ad, r);
-                                ptx::tmem_wait_ld();
+                        for (int c = 0; c < 4 * (C::NP / R); ++c) {
+                            uint32_t r[HC];
+                            const uint32_t ad = lane_addr + C::kColO + c * R + c0;
+                            tmem_ld(ad, r);
+                            ptx::tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < HC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha[i]);
-                                tmem_st(ad, r);
-                            }
+                            for (int i = 0; i < HC; ++i)
+                                r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, alpha, i));
+                            tmem_st(ad, r);
+                        }
                         ptx::tmem_wait_st();
                     }
                 }
@@ -685,28 +718,25 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 uint8_t* prow = ropes + (g % NR) * kRopeBytes + tok * 64;
                 const int sw = (tok >> 1) & 3;
                 if (C::kTwoPass) {
-                    if (g > 0 && !uwait(lo_free, (g - 1) & 1)) { ok = false; break; }
-                    uint8_t* lrow = plo + tok * 64;
-#pragma unroll
-                    for (int u = 0; u < HC / 16; ++u) {
-                        const int at = ((half * 2 + u) ^ sw) << 4;
-                        *(uint4*)(prow + at) = make_uint4(hi8[4 * u], hi8[4 * u + 1], hi8[4 * u + 2], hi8[4 * u + 3]);
-                        *(uint4*)(lrow + at) = make_uint4(lo8[4 * u], lo8[4 * u + 1], lo8[4 * u + 2], lo8[4 * u + 3]);
-                    }
+                    // one buffer for the lo terms: O of the tile before is done with it
+                    if (g > 0 && !uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
+                    const int at = tok * 64 + ((grp ^ sw) << 4);
+                    *(uint4*)(ropes + (g % NR) * kRopeBytes + at) = make_uint4(hi8[0], hi8[1], hi8[HC / 8], hi8[HC / 4 - 1]);
+                    *(uint4*)(plo + at) = make_uint4(lo8[0], lo8[1], lo8[HC / 8], lo8[HC / 4 - 1]);
                 } else if (R == 32) {
-                    *(uint4*)(prow + ((half ^ sw) << 4)) = make_uint4(hi8[0], hi8[1], hi8[HC / 8], hi8[HC / 4 - 1]);
-                    *(uint4*)(prow + (((2 + half) ^ sw) << 4)) = make_uint4(lo8[0], lo8[1], lo8[HC / 8], lo8[HC / 4 - 1]);
+                    *(uint4*)(prow + ((grp ^ sw) << 4)) = make_uint4(hi8[0], hi8[1], hi8[HC / 8], hi8[HC / 4 - 1]);
+                    *(uint4*)(prow + (((2 + grp) ^ sw) << 4)) = make_uint4(lo8[0], lo8[1], lo8[HC / 8], lo8[HC / 4 - 1]);
                 } else {
-                    *(uint2*)(prow + ((0 ^ sw) << 4) + 8 * half) = make_uint2(hi8[0], hi8[1]);
-                    *(uint2*)(prow + ((1 ^ sw) << 4) + 8 * half) = make_uint2(lo8[0], lo8[1]);
+                    *(uint2*)(prow + ((0 ^ sw) << 4) + 8 * grp) = make_uint2(hi8[0], hi8[1]);
+                    *(uint2*)(prow + ((1 ^ sw) << 4) + 8 * grp) = make_uint2(lo8[0], lo8[1]);
                 }
                 if (edge) {
                     // Rows that some row of the group must not see may hold NaN codes (what lies
                     // behind the sequence's end, a later token's row), and 0 x NaN is NaN: those
                     // codes become 0.  A row that does see them has NaN scores already.
                     const int n0 = max(sg.kmin - j * kT, 0);
-                    const int tid = threadIdx.x - 64;   // 0 .. 255
-                    for (int e = tid; e < (kT - n0) * 32; e += 256) {
+#pragma unroll 1
+                    for (int e = threadIdx.x - kRoleThreads; e < (kT - n0) * 32; e += C::kSoft) {
                         const int r = n0 + (e >> 5), c = (e >> 3) & 3, u = e & 7;
                         uint4* at = (uint4*)(chunks + ((4 * g + c) % NC) * kChunkBytes + r * 128) + u;
                         uint4 v = *at;
@@ -739,24 +769,24 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 }
             }
             // row held by this lane: the lane bits from 16 down, as many as HC has
-            const int my_row = lane >> (HC == 32 ? 0 : HC == 16 ? 1 : 2);
-            float* sums = tops + half * 128;   // [4 quarters][32]
-            __syncwarp();
-            sums[quad * 32 + my_row] = l[0];
-            if (lane == 0) out_scale[half * 4 + quad] = s_top;
+            const int my_row = lane >> (HC == 16 ? 1 : 2);
+            float* sums = (float*)(red + grp * 16);   // [4 quarters][16]
+            meet();   // red is read
+            if (!ok) break;
+            sums[quad * 16 + my_row] = l[0];
+            if (lane == 0) out_scale[grp * 4 + quad] = s_top;
             meet();
             if (!ok) break;
-            const float* st4 = out_scale + half * 4;
+            const float* st4 = out_scale + grp * 4;
             const float s_out0 = fmaxf(fmaxf(st4[0], st4[1]), fmaxf(st4[2], st4[3]));
             const float s_out = s_out0 > 0.f ? s_out0 : 1.f;
             if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
             ptx::tc_fence_after();
-            float f[HC];
-#pragma unroll
-            for (int i = 0; i < HC; ++i) {
-                const float t = (sums[i] + sums[32 + i]) + (sums[64 + i] + sums[96 + i]);
-                f[i] = t != 0.f ? (s_ref / s_out) / t : 0.f;
-                if (quad == 0 && lane == i) ws.part_ml[(size_t)sg.slot * R + c0 + i] = make_float4(M[i], t, s_out, 0.f);
+            float f = 0.f;   // lane i: what turns row c0 + i of O into its normalised output
+            if (lane < HC) {
+                const float t = (sums[lane] + sums[16 + lane]) + (sums[32 + lane] + sums[48 + lane]);
+                f = t != 0.f ? (s_ref / s_out) / t : 0.f;
+                if (quad == 0) ws.part_ml[(size_t)sg.slot * R + c0 + lane] = make_float4(m_row, t, s_out, 0.f);
             }
             __half* po = ws.part_o + ((size_t)sg.slot * R + c0) * kDc + tok;
 #pragma unroll 1
@@ -773,16 +803,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     ptx::tmem_wait_ld();
                 }
 #pragma unroll
-                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(__uint_as_float(r[i]) * f[i]);
+                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, f, i));
             }
             ptx::tc_fence_before();
-            meet();   // the sums are read before the next piece's references come in their place
-            sg = nxt;
-            have = more;
+            meet();   // the sums are read
             ++piece;
         }
         if (!ok) fail(err, abort_flag, 13);
-        if (loader && q_loads > 0) ptx::mbar_wait(q_full, (q_loads - 1) & 1, nullptr);   // in flight after an abort
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -1147,7 +1174,7 @@ cudaError_t launch_attn(const CUtensorMap& ml, const CUtensorMap& mr, const Src&
                         DevErr err, cudaStream_t st) {
     cudaError_t e = set_smem(attn_kernel<R>, Cfg<R>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_kernel<R>, dim3(src.s.ctas), dim3(kThreads), Cfg<R>::kSmem, st, ml, mr, src, p.block_table,
+    return launch_pdl(attn_kernel<R>, dim3(src.s.ctas), dim3(Cfg<R>::kThreads), Cfg<R>::kSmem, st, ml, mr, src, p.block_table,
                       p.scales, p.num_pages, p.scale * 1.4426950408889634f, ws, err);
 }
 
