@@ -69,35 +69,32 @@ template <int R> struct Cfg {
     static_assert(kSmem <= 232448, "shared memory over the 227 KB limit");
 };
 
-// tcgen05.mma kind::f8f6f4, both operands in shared memory, issued by the lane whose `lead` is
-// set.  The whole warp runs the issue loops with warp-uniform values, so that descriptors stay
-// in uniform registers: from one thread's branch, each product took ~105 cycles to issue, twice
-// what the smallest ones take to run.  Only the low words of the descriptors (address,
-// leading offset) vary.
-__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                       uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp.  Asynchronous instructions (products, commits, bulk and TMA
+// copies) are issued under this predicate: it tells the compiler that one lane is active, where
+// a test of the lane number makes it loop over the active lanes around each of them (a product
+// then took some twenty instructions, which four softmax warps per scheduler stretched to ~90
+// cycles).
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+// tcgen05.mma kind::f8f6f4, both operands in shared memory
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
         "mov.b64 da, {%1, %2};\n\t"
         "mov.b64 db, {%3, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(lead)
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // A value that is the same in all lanes, as one the compiler knows to be so (loops around the
 // products run on it)
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 __device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x); }
-__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar)),
-        "r"(lead)
-        : "memory");
-}
 // Descriptor words: low = address and leading offset (both / 16), high = stride offset / 16,
 // version 1, swizzle (2: 128 bytes, 4: 64 bytes)
 __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle << 29); }
@@ -232,7 +229,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
     return false;
 }
 
-__device__ __forceinline__ void fail(DevErr err, volatile int* abort_flag, int where) {
+__device__ __noinline__ void fail(DevErr err, volatile int* abort_flag, int where) {
     latch(err, kErrTimeout, (long long)where * 1000000 + blockIdx.x);
     *abort_flag = 1;
 }
@@ -315,8 +312,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     long long total = 0;
     {
         long long mine = 0;
+#pragma unroll 1
         for (int i = threadIdx.x; i < nv; i += kThreads) mine += cost_of(tiles_of(src.vlen(i)));
         if (blockIdx.x == 0)
+#pragma unroll 1
             for (int b = threadIdx.x; b < src.s.B; b += kThreads)
                 if (src.raw_len(b) < 0) latch(err, kErrOutOfRange, b);
 #pragma unroll
@@ -338,6 +337,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     if (blockIdx.x == 0 && threadIdx.x == 0) ws.plan[0] = per;
     if (lo < total || blockIdx.x == 0) {
         long long carry = 0;
+#pragma unroll 1
         for (int c0 = 0; c0 < nv; c0 += kThreads) {
             const int i = c0 + (int)threadIdx.x;
             const long long cb = i < nv ? cost_of(tiles_of(src.vlen(i))) : 0;
@@ -402,14 +402,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         // lane l holds the page (and its scale) of block base + l of the sequence
         const uint64_t policy = src.s.G > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
         const long long none = num_pages * kPageRows;   // a box past the last row reads zeros
-        uint32_t g = 0, cn = 0;                         // tiles, chunks requested
+        uint32_t g = 0, cn = 0, slot = 0, use = 0;      // tiles and chunks requested, next slot and its uses
         bool ok = true;
         while (ok && next_piece()) {
             const int blocks = (sg.len + kPageRows - 1) / kPageRows;
             long long row = none;
             float sc = 0.f;
 #pragma unroll 1
-            for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+            for (int j = sg.j0; ok && j < sg.j1; ++j) {
                 const int at = (j - sg.j0) & 15;
                 if (at == 0) {
                     const int blk = 2 * j + lane;
@@ -422,44 +422,42 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 }
                 const int r0 = (int)__shfl_sync(0xffffffffu, row, 2 * at), r1 = (int)__shfl_sync(0xffffffffu, row, 2 * at + 1);
                 const float s0 = __shfl_sync(0xffffffffu, sc, 2 * at), s1 = __shfl_sync(0xffffffffu, sc, 2 * at + 1);
-                if (lane == 0) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c, ++cn) {
-                        const uint32_t slot = cn % NC, use = cn / NC;
-                        if (ok && use > 0 && !ptx::mbar_wait(&chunk_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
-                        if (!ok) break;
+                for (int c = 0; c < 4; ++c) {
+                    if (ok && use > 0 && !wait_warp(&chunk_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
+                    if (ok && elect()) {
                         uint8_t* dst = chunks + slot * kChunkBytes;
                         ptx::mbar_expect_tx(&chunk_full[slot], kChunkBytes);
                         ptx::tma_load_2d_hint(dst, &tm_lat, &chunk_full[slot], 128 * c, r0, policy);
                         ptx::tma_load_2d_hint(dst + kChunkBytes / 2, &tm_lat, &chunk_full[slot], 128 * c, r1, policy);
                     }
-                    const uint32_t slot = g % NR, use = g / NR;
-                    if (ok && use > 0 && !ptx::mbar_wait(&rope_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
-                    if (ok) {
-                        page_scale[2 * (g & 3)] = s0;
-                        page_scale[2 * (g & 3) + 1] = s1;
-                        uint8_t* dst = ropes + slot * kRopeBytes;
-                        ptx::mbar_expect_tx(&rope_full[slot], kRopeBytes);
-                        ptx::tma_load_2d_hint(dst, &tm_rope, &rope_full[slot], kDc, r0, policy);
-                        ptx::tma_load_2d_hint(dst + kRopeBytes / 2, &tm_rope, &rope_full[slot], kDc, r1, policy);
-                    } else {
-                        --g;   // this tile's rotary columns were not requested
-                    }
+                    cn += ok;
+                    if (++slot == NC) slot = 0, ++use;
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (ok && g >= NR && !wait_warp(&rope_empty[g % NR], (g / NR - 1) & 1, abort_flag)) ok = false;
+                if (ok && elect()) {
+                    page_scale[2 * (g & 3)] = s0;
+                    page_scale[2 * (g & 3) + 1] = s1;
+                    uint8_t* dst = ropes + (g % NR) * kRopeBytes;
+                    ptx::mbar_expect_tx(&rope_full[g % NR], kRopeBytes);
+                    ptx::tma_load_2d_hint(dst, &tm_rope, &rope_full[g % NR], kDc, r0, policy);
+                    ptx::tma_load_2d_hint(dst + kRopeBytes / 2, &tm_rope, &rope_full[g % NR], kDc, r1, policy);
+                }
+                g += ok;
             }
         }
+        if (!ok) fail(err, abort_flag, 11);
         if (lane == 0) {
-            if (!ok) fail(err, abort_flag, 11);
             // loads still in flight (after an abort) land before the CTA leaves
+#pragma unroll 1
             for (uint32_t k = 0; k < (uint32_t)NC && k < cn; ++k)
                 ptx::mbar_wait(&chunk_full[(cn - 1 - k) % NC], ((cn - 1 - k) / NC) & 1, nullptr);
+#pragma unroll 1
             for (uint32_t k = 0; k < (uint32_t)NR && k < g; ++k)
                 ptx::mbar_wait(&rope_full[(g - 1 - k) % NR], ((g - 1 - k) / NR) & 1, nullptr);
         }
     } else if (warp == 1) {
         // ---------------------------------------------- queries and score products
-        const uint32_t lead = lane == 0;
         constexpr uint32_t idesc = idesc_e4m3(128, 2 * R, 0, 0);
         constexpr uint32_t h128 = desc_hi(1024, 2), h64 = desc_hi(512, 4);
         const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), 16), rope0 = desc_lo(ptx::smem_u32(ropes), 16),
@@ -472,7 +470,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             // Every softmax thread has read the last scores: their products are done with the
             // queries, and it is done with the row scales.
             if (g > 0 && !wait(&s_free[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
-            if (lead) {
+            if (elect()) {
                 ptx::mbar_expect_tx(q_full, C::kQBytes + R * 4);
                 const uint8_t* from = ws.q_img + (size_t)sg.item * C::kQBytes;
                 for (int o = 0; o < C::kQBytes; o += C::kQBytes / 4)
@@ -492,24 +490,27 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     if (!wait(&chunk_full[slot], use & 1)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const uint32_t a = chunk0 + slot * (kChunkBytes >> 4), b = q0 + c * (2 * R * 128 >> 4);
+                    if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_f8(lead, d, a + 2 * k, h128, b + 2 * k, h128, idesc, (c | k) != 0);
+                        for (int k = 0; k < 4; ++k) mma_f8(d, a + 2 * k, h128, b + 2 * k, h128, idesc, (c | k) != 0);
+                    }
                     if (++slot == NC) slot = 0, ++use;
                 }
                 if (!ok || !wait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t a = rope0 + (g % NR) * (kRopeBytes >> 4), b = q0 + 4 * (2 * R * 128 >> 4);
+                if (elect()) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) mma_f8(lead, d, a + 2 * k, h64, b + 2 * k, h64, idesc, 1);
-                commit(lead, &s_full[g & 1]);
+                    for (int k = 0; k < 2; ++k) mma_f8(d, a + 2 * k, h64, b + 2 * k, h64, idesc, 1);
+                    ptx::mma_commit(&s_full[g & 1]);
+                }
             }
         }
-        if (!ok && lead) fail(err, abort_flag, 12);
-        commit(lead, drain);
-        if (!ptx::mbar_wait(drain, 0, nullptr) && lead) fail(err, abort_flag, 14);
+        if (!ok) fail(err, abort_flag, 12);
+        if (elect()) ptx::mma_commit(drain);
+        if (!ptx::mbar_wait(drain, 0, nullptr)) fail(err, abort_flag, 14);
     } else if (warp == 2) {
         // ---------------------------------------------------------- O products
-        const uint32_t lead = lane == 0;
         constexpr uint32_t idesc = idesc_e4m3(128, C::NP, 1, 1);
         constexpr uint32_t h128 = desc_hi(1024, 2), h64 = desc_hi(512, 4);
         const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), kChunkBytes), rope0 = desc_lo(ptx::smem_u32(ropes), 512),
@@ -524,28 +525,32 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 ptx::tc_fence_after();
                 const uint32_t p = rope0 + (g % NR) * (kRopeBytes >> 4);
                 // chunk by chunk, so that the first slots are free for the next loads early
+                if (elect()) {
+                    uint32_t slot = slot0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t a = chunk0 + slot0 * (kChunkBytes >> 4), d = tmem + C::kColO + c * C::NP;
-#pragma unroll
-                    for (int k = 0; k < kT / 32; ++k)
-                        mma_f8(lead, d, a + 256 * k, h128, p + 128 * k, h64, idesc, acc0 | (k > 0));
-                    if (C::kTwoPass) {
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t a = chunk0 + slot * (kChunkBytes >> 4), d = tmem + C::kColO + c * C::NP;
 #pragma unroll
                         for (int k = 0; k < kT / 32; ++k)
-                            mma_f8(lead, d, a + 256 * k, h128, lo0 + 128 * k, h64, idesc, 1);
+                            mma_f8(d, a + 256 * k, h128, p + 128 * k, h64, idesc, acc0 | (k > 0));
+                        if (C::kTwoPass) {
+#pragma unroll
+                            for (int k = 0; k < kT / 32; ++k)
+                                mma_f8(d, a + 256 * k, h128, lo0 + 128 * k, h64, idesc, 1);
+                        }
+                        ptx::mma_commit(&chunk_empty[slot]);
+                        slot = slot + 1 == NC ? 0 : slot + 1;
                     }
-                    commit(lead, &chunk_empty[slot0]);
-                    if (++slot0 == NC) slot0 = 0;
+                    ptx::mma_commit(&o_done[g & 1]);
+                    ptx::mma_commit(&rope_empty[g % NR]);
                 }
-                commit(lead, &o_done[g & 1]);
-                commit(lead, &rope_empty[g % NR]);
+                slot0 = (slot0 + 4) % NC;
                 acc0 = 1;
             }
         }
-        if (!ok && lead) fail(err, abort_flag, 16);
-        commit(lead, drain);
-        if (!ptx::mbar_wait(drain, 0, nullptr) && lead) fail(err, abort_flag, 17);
+        if (!ok) fail(err, abort_flag, 16);
+        if (elect()) ptx::mma_commit(drain);
+        if (!ptx::mbar_wait(drain, 0, nullptr)) fail(err, abort_flag, 17);
     } else if (warp >= kRoleThreads / 32) {
         // ------------------------------------------------- softmax and epilogue
         const int quad = warp & 3, grp = (warp - kRoleThreads / 32) >> 2;
