@@ -174,10 +174,9 @@ struct Src {
     // keys of new token t of a sequence with L tokens
     __device__ int keys(int L, int t) const { return L - (s.q_len - 1 - t); }
     __device__ int vseqs() const { return s.sib > 1 ? s.B : s.B * s.G; }
-    __device__ int vlen(int i) const {
-        if (s.sib > 1) return len(i);
-        return max(keys(len(i / s.G), last_token(i % s.G)), 0);
-    }
+    __device__ int vseq_b(int i) const { return s.sib > 1 ? i : i / s.G; }
+    // what virtual sequence i is charged for, its sequence having L tokens
+    __device__ int vkeys(int L, int i) const { return s.sib > 1 ? L : max(keys(L, last_token(i % s.G)), 0); }
 };
 
 __device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kT - 1) / kT : 0; }
@@ -191,21 +190,23 @@ static_assert(sizeof(Seg) % 16 == 0, "alignment of what lies behind");
 // Walks the pieces of this CTA's range.  Positions are counted from the range's start.
 struct SegIter {
     const Src& src;
-    int span;   // cost units of the range
-    int cs;     // where virtual sequence i's cost starts (not above 0 at first)
     int i;
+    int cs;     // where virtual sequence i's cost starts (not above 0 at first)
+    int span;   // cost units of the range
+    int len;    // tokens of sequence i's sequence, or -1: look
     __device__ bool next(Seg& s) {
         const int nv = src.vseqs();
         while (i < nv && cs < span) {
             const int ii = i++;
-            const int n = tiles_of(src.vlen(ii));
+            s.b = src.s.sib > 1 ? ii : ii / src.s.G;
+            s.g = src.s.sib > 1 ? (int)blockIdx.x % src.s.sib : ii - s.b * src.s.G;
+            s.len = len >= 0 ? len : src.len(s.b);
+            len = -1;
+            const int n = tiles_of(src.vkeys(s.len, ii));
             const int f = cs + kPieceCost;
             cs += (int)cost_of(n);
             if (n == 0) continue;
-            s.b = src.s.sib > 1 ? ii : ii / src.s.G;
-            s.g = src.s.sib > 1 ? (int)blockIdx.x % src.s.sib : ii % src.s.G;
             s.item = s.b * src.s.G + s.g;
-            s.len = src.len(s.b);
             s.kmin = src.keys(s.len, src.first_token(s.g));
             s.kmax = src.keys(s.len, src.last_token(s.g));
             s.j0 = max(-f, 0);
@@ -267,10 +268,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
     static_assert(64 * 4 + 64 * 16 + 64 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
     static_assert(NC % 2 == 0, "16-byte alignment of the words behind the barriers");
-    // the planning's scratch lies where the reductions come later
-    long long* plan_wsum = (long long*)red;             // [kThreads / 32]
-    long long* plan_first = plan_wsum + 32;             // [2]
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NC; ++i) {
@@ -303,74 +300,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     }
     if (threadIdx.x == 0) pdl_trigger();
 
-    // ---- planning: total cost, then the virtual sequence that holds this CTA's first unit.
-    // The call's first kernel waits for all earlier work before it lets this one launch, so
-    // lengths, table and cache are final.
-    constexpr int kWarps = kThreads / 32;
-    const int nv = src.vseqs(), ranges = src.s.ctas / src.s.sib;
-    const int range = (int)blockIdx.x / src.s.sib;
-    long long total = 0;
-    {
-        long long mine = 0;
-#pragma unroll 1
-        for (int i = threadIdx.x; i < nv; i += kThreads) mine += cost_of(tiles_of(src.vlen(i)));
-        if (blockIdx.x == 0)
-#pragma unroll 1
-            for (int b = threadIdx.x; b < src.s.B; b += kThreads)
-                if (src.raw_len(b) < 0) latch(err, kErrOutOfRange, b);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) plan_wsum[warp] = mine;
-        if (threadIdx.x == 0) {
-            plan_first[0] = nv;
-            plan_first[1] = 0;
-        }
-        ptx::tc_fence_before();
-        __syncthreads();
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) total += plan_wsum[i];
-        __syncthreads();
-    }
-    const long long per = total > 0 ? (total + ranges - 1) / ranges : 1;
-    const long long lo = range < ranges ? min(total, range * per) : total, hi = min(total, lo + per);
-    if (blockIdx.x == 0 && threadIdx.x == 0) ws.plan[0] = per;
-    if (lo < total || blockIdx.x == 0) {
-        long long carry = 0;
-#pragma unroll 1
-        for (int c0 = 0; c0 < nv; c0 += kThreads) {
-            const int i = c0 + (int)threadIdx.x;
-            const long long cb = i < nv ? cost_of(tiles_of(src.vlen(i))) : 0;
-            long long incl = cb;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) plan_wsum[warp] = incl;
-            __syncthreads();
-            long long before = carry, chunk = 0;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const long long v = plan_wsum[k];
-                before += k < warp ? v : 0;
-                chunk += v;
-            }
-            const long long cs = before + incl - cb;
-            if (i < nv) {
-                if (cb > 0 && cs <= lo && lo < cs + cb) {   // unique: the region that holds lo
-                    plan_first[0] = i;
-                    plan_first[1] = cs;
-                }
-                if (blockIdx.x == 0) ws.plan[1 + i] = cs;   // for the merge
-            }
-            carry += chunk;
-            __syncthreads();
-        }
-    }
-    SegIter it{src, (int)(hi - lo), (int)(plan_first[1] - lo), (int)plan_first[0]};
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-    __syncthreads();   // plan_first is read before red is written
 
     // The pieces, in order, as every role sees them: warp 3 finds them ahead of time
     Seg sg;
@@ -385,6 +318,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         return uniform(sg.j0 < sg.j1);
     };
     if (warp == 3) {
+        pdl_wait();   // the previous kernel of this call planned, and all before it is done
+        const int4 start = ws.start[blockIdx.x / src.s.sib];
+        SegIter it{src, start.x, start.y, start.z, start.w};
         bool more = true;
 #pragma unroll 1
         for (uint32_t n = 0; more; ++n) {
@@ -421,7 +357,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     if (!good && blk < blocks && blk < 2 * sg.j1) latch(err, kErrOutOfRange, sg.b);
                 }
                 const int r0 = (int)__shfl_sync(0xffffffffu, row, 2 * at), r1 = (int)__shfl_sync(0xffffffffu, row, 2 * at + 1);
-                const float s0 = __shfl_sync(0xffffffffu, sc, 2 * at), s1 = __shfl_sync(0xffffffffu, sc, 2 * at + 1);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (ok && use > 0 && !wait_warp(&chunk_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
@@ -434,6 +369,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     cn += ok;
                     if (++slot == NC) slot = 0, ++use;
                 }
+                // the scales may still be on their way here, which must not hold up the loads above
+                const float s0 = __shfl_sync(0xffffffffu, sc, 2 * at), s1 = __shfl_sync(0xffffffffu, sc, 2 * at + 1);
                 if (ok && g >= NR && !wait_warp(&rope_empty[g % NR], (g / NR - 1) & 1, abort_flag)) ok = false;
                 if (ok && elect()) {
                     page_scale[2 * (g & 3)] = s0;
@@ -793,7 +730,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 f = t != 0.f ? (s_ref / s_out) / t : 0.f;
                 if (quad == 0) ws.part_ml[(size_t)sg.slot * R + c0 + lane] = make_float4(m_row, t, s_out, 0.f);
             }
+            // (a warp's store is 64 contiguous bytes; turning the tile around with shuffles for
+            // 16-byte stores took longer)
             __half* po = ws.part_o + ((size_t)sg.slot * R + c0) * kDc + tok;
+            float fr[HC];
+#pragma unroll
+            for (int i = 0; i < HC; ++i) fr[i] = __shfl_sync(0xffffffffu, f, i);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t r[HC];
@@ -808,7 +750,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     ptx::tmem_wait_ld();
                 }
 #pragma unroll
-                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, f, i));
+                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(__uint_as_float(r[i]) * fr[i]);
             }
             ptx::tc_fence_before();
             meet();   // the sums are read
@@ -822,15 +764,18 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ the queries
-// q_lat[v, h, :] = W_UK[h]^T q_nope[v, h, :] for 128 queries v = (b, t) of one head, as
-// D [128 queries x 512] = Q_h [128 x 128] . W_UK^T[h]^T, so that a query is a TMEM lane and the
-// four warps of a lane quarter hold its 512 values: the row [q_lat | q_rope] gets one
-// power-of-two scale that puts its largest value in (224, 448], and leaves as the two E4M3
-// terms in the shared-memory image the attention kernel loads whole.
-// One CTA per (head, 128 queries): the 128 KB of W_UK^T[h] bound it.
-constexpr int kAbsorbThreads = 512;
-constexpr int kAbsorbA = 2 * 128 * 128, kAbsorbB = 4 * 256 * 128;
-constexpr int kAbsorbSmem = kAbsorbA + kAbsorbB + 4 * 128 * 4 + 64 + 1024;
+// q_lat[v, h, :] = W_UK[h]^T q_nope[v, h, :] for 128 queries v = (b, t) of one head.  A cluster
+// of two CTAs shares a (head, 128 queries): CTA r makes latent columns 256 r ..., as
+// D [128 queries x 256] = Q_h [128 x 128] . W_UK^T[h][256 r ..]^T, and takes rotary columns 32 r ...
+// A query is a TMEM lane; its largest value is agreed on through distributed shared memory,
+// and the row [q_lat | q_rope] gets one power-of-two scale that puts that value in (224, 448].
+// It leaves as two E4M3 terms in the shared-memory image the attention kernel loads whole.
+// Latency bounds it.  One CTA per head took 6.1 us of a one-sequence step; a cluster of four
+// is as quick as this one, but 128 heads' 512 CTAs need a second wave, and the attention
+// kernel may start only when the last of them has.
+constexpr int kAbsorbThreads = 512, kAbsorbCluster = 2;
+constexpr int kAbsorbA = 2 * 128 * 128, kAbsorbB = 2 * 256 * 128;
+constexpr int kAbsorbSmem = kAbsorbA + kAbsorbB + 5 * 128 * 4 + 64 + 1024;
 
 // smallest e with amax <= 448 * 2^e (0 for 0), not below -100
 __device__ __forceinline__ int query_exponent(float amax) {
@@ -840,31 +785,124 @@ __device__ __forceinline__ int query_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-__device__ __forceinline__ void split_e4m3(const float (&x)[16], float inv, uint4& hi, uint4& lo) {
-    uint32_t h[8], t[8];
+// 2 n values times inv -> n words' worth of hi and lo codes (two codes per 16 bits)
+template <int N>
+__device__ __forceinline__ void split_e4m3(const float (&x)[2 * N], float inv, uint32_t (&hi)[N / 2], uint32_t (&lo)[N / 2]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
-        h[i] = e4m3x2_f32(a, b);
-        const uint32_t f = f16x2_of_e4m3(h[i]);
+        const uint32_t h = e4m3x2_f32(a, b), f = f16x2_of_e4m3(h);
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-        t[i] = e4m3x2_f32(a - v.x, b - v.y);
+        const uint32_t t = e4m3x2_f32(a - v.x, b - v.y);
+        hi[i / 2] = i % 2 ? hi[i / 2] | h << 16 : h;
+        lo[i / 2] = i % 2 ? lo[i / 2] | t << 16 : t;
     }
-    hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    lo = make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
 }
 
-__global__ void __launch_bounds__(kAbsorbThreads, 1)
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {   // the same place in CTA `rank`
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\tld.shared::cluster.f32 %0, [ra];\n\t}"
+        : "=f"(v)
+        : "r"(ptx::smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// The work split, by one CTA beside those that make the queries: for every range the virtual
+// sequence that holds its first unit (ws.start), for every item where its pieces' partials
+// lie (ws.pieces).
+__device__ void plan(const Src& src, const Ws& ws, DevErr err) {
+    __shared__ long long wsum[kAbsorbThreads / 32];
+    constexpr int kWarps = kAbsorbThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Shape& s = src.s;
+    const int nv = src.vseqs(), ranges = s.ctas / s.sib;
+    // lengths of the first 512 virtual sequences stay in registers
+    const int len0 = (int)threadIdx.x < nv ? src.len(src.vseq_b(threadIdx.x)) : 0;
+    auto length = [&](int i) { return i < kAbsorbThreads ? len0 : src.len(src.vseq_b(i)); };
+    long long mine = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < nv; i += kAbsorbThreads) mine += cost_of(tiles_of(src.vkeys(length(i), i)));
+#pragma unroll 1
+    for (int b = threadIdx.x; b < s.B; b += kAbsorbThreads)
+        if (src.raw_len(b) < 0) latch(err, kErrOutOfRange, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) wsum[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) total += wsum[i];
+    const long long per = total > 0 ? (total + ranges - 1) / ranges : 1;
+    // ranges without work
+    for (int r = threadIdx.x; r < s.ctas; r += kAbsorbThreads)
+        if (r >= ranges || r * per >= total) ws.start[r] = make_int4(nv, 0, 0, -1);
+    long long carry = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < nv; c0 += kAbsorbThreads) {
+        const int i = c0 + (int)threadIdx.x, L = i < nv ? length(i) : 0;
+        const int n = i < nv ? tiles_of(src.vkeys(L, i)) : 0;
+        const long long cb = cost_of(n);
+        long long incl = cb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        __syncthreads();
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        long long before = carry;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const long long v = wsum[k];
+            before += k < warp ? v : 0;
+            carry += v;
+        }
+        const long long cs = before + incl - cb;
+        if (i < nv) {
+            // the ranges that start in [cs, cs + cb)
+#pragma unroll 1
+            for (long long r = (cs + per - 1) / per; r * per < cs + cb && r < ranges; ++r)
+                ws.start[r] = make_int4(i, (int)(cs - r * per), (int)min(per, total - r * per), L);
+            const long long f = cs + kPieceCost, r0 = f / per;
+            const int at = (int)(f - r0 * per);   // place of the first tile in its range
+#pragma unroll 1
+            for (int k = 0; k < (s.sib > 1 ? s.G : 1); ++k) {
+                const int item = s.sib > 1 ? i * s.G + k : i, g = s.sib > 1 ? k : i % s.G;
+                const int nt = n > 0 ? tiles_of(src.keys(L, src.last_token(g))) : 0;
+                const int np = nt > 0 ? (int)((at + nt - 1) / per) + 1 : 0;
+                // slot of piece p > 0: .x + (p - 1) sib
+                ws.pieces[item] = make_int2((int)(s.B * s.G + (r0 + 1) * s.sib + (s.sib > 1 ? k : 0)), np);
+            }
+        }
+    }
+}
+
+__global__ void __cluster_dims__(kAbsorbCluster, 1, 1) __launch_bounds__(kAbsorbThreads, 2)
 absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_w,
-              const __nv_bfloat16* __restrict__ q_rope, const Shape s, const Ws ws, const DevErr err) {
+              const __nv_bfloat16* __restrict__ q_rope, const Src src, const Ws ws, const DevErr err) {
+    const Shape& s = src.s;
+    if (blockIdx.x >= kAbsorbCluster * s.H) {   // a cluster apart: uniform
+        pdl_wait();
+        if (threadIdx.x == 0) pdl_trigger();
+        if (blockIdx.x == kAbsorbCluster * s.H && blockIdx.y == 0) plan(src, ws, err);
+        return;
+    }
     extern __shared__ uint8_t absorb_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)absorb_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + kAbsorbA;
     float* s_max = (float*)(sB + kAbsorbB);   // [4 column groups][128]
-    uint64_t* full = (uint64_t*)(s_max + 512);
+    float* s_row = s_max + 512;               // [128] this CTA's largest value of each query
+    uint64_t* full = (uint64_t*)(s_row + 128);
     uint64_t* d_full = full + 1;
     uint32_t* tmem_slot = (uint32_t*)(d_full + 1);
-    const int h = blockIdx.x, v0 = blockIdx.y * 128, NV = s.B * s.q_len;
+    const int h = blockIdx.x / kAbsorbCluster, rank = blockIdx.x % kAbsorbCluster;
+    const int v0 = blockIdx.y * 128, NV = s.B * s.q_len;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, cg = warp >> 2;
     if (threadIdx.x == 0) {
         ptx::mbar_init(full, 1);
@@ -873,69 +911,66 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         ptx::mbar_expect_tx(full, kAbsorbA + kAbsorbB);
         // the weights first: earlier kernels do not write them
 #pragma unroll
-        for (int kc = 0; kc < 2; ++kc)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-                ptx::tma_load_2d(sB + (2 * kc + n) * 32768, &tm_w, full, 64 * kc, h * kDc + 256 * n);
+        for (int kc = 0; kc < 2; ++kc) ptx::tma_load_2d(sB + kc * 32768, &tm_w, full, 64 * kc, h * kDc + 256 * rank);
         pdl_wait();      // all earlier work is done
         pdl_trigger();   // only now may the next kernel launch
 #pragma unroll
         for (int kc = 0; kc < 2; ++kc) ptx::tma_load_3d(sA + kc * 16384, &tm_q, full, 64 * kc, v0, h);
     }
     if (warp == 1) {
-        ptx::tmem_alloc(tmem_slot, 512);
+        ptx::tmem_alloc(tmem_slot, 256);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    if (threadIdx.x == 32) {
-        if (!ptx::mbar_wait(full, 0, nullptr)) {
-            latch(err, kErrTimeout, 9200000 + h);
-        } else {
-            ptx::tc_fence_after();
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    if (warp == 1) {
+        const bool landed = ptx::mbar_wait(full, 0, nullptr);
+        if (!landed) latch(err, kErrTimeout, 9200000 + h);
+        ptx::tc_fence_after();
+        if (elect()) {
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, 256, 0, 0);
+            if (landed) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int kc = 0; kc < 2; ++kc)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + 256 * n, ptx::desc_kmajor_sw128(ptx::smem_u32(sA + kc * 16384) + 32 * k),
-                                    ptx::desc_kmajor_sw128(ptx::smem_u32(sB + (2 * kc + n) * 32768) + 32 * k), idesc,
-                                    (kc | k) != 0);
+                for (int k = 0; k < 8; ++k) {
+                    ptx::mma_ss(tmem, ptx::desc_kmajor_sw128(ptx::smem_u32(sA) + (k >> 2) * 16384 + 32 * (k & 3)),
+                                ptx::desc_kmajor_sw128(ptx::smem_u32(sB) + (k >> 2) * 32768 + 32 * (k & 3)), idesc, k != 0);
+                }
+            }
+            ptx::mma_commit(d_full);   // after a timeout nothing was issued and this completes at once
         }
-        ptx::mma_commit(d_full);   // after a timeout nothing was issued and this completes at once
+        __syncwarp();
     }
-    __syncwarp();
     const int v = v0 + 32 * quad + lane;
     const bool warp_on = v0 + 32 * quad < NV, on = v < NV;
-    const uint32_t src_col = tmem + ((uint32_t)(32 * quad) << 16) + 128 * cg;
-    // this warp group's 16 rotary columns; they may come from the previous kernel
+    const uint32_t src_col = tmem + ((uint32_t)(32 * quad) << 16) + 64 * cg;
+    // this warp's 8 rotary columns; they may come from the previous kernel
     pdl_wait();
-    float rope[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) rope[i] = 0.f;
+    float rope[8] = {};
     if (on) {
-        const uint4* r = (const uint4*)(q_rope + ((size_t)v * s.H + h) * kDr + 16 * cg);
-        const uint4 a = r[0], b = r[1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint4 a = *(const uint4*)(q_rope + ((size_t)v * s.H + h) * kDr + 32 * rank + 8 * cg);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             rope[2 * i] = __uint_as_float(w[i] << 16);
             rope[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
+    // where the row goes (divisions off the critical path)
+    const int R = s.R, b = v / s.q_len, t = v - b * s.q_len, row = t * s.H + h, g = row / R, rh = row - g * R, rl = R + rh;
+    const size_t img = (size_t)2 * R * kRow, item = (size_t)b * s.G + g;
+    uint8_t* chunk = ws.q_img + item * img + (size_t)(2 * rank + (cg >> 1)) * (2 * R * 128);
+    uint8_t* rp = ws.q_img + item * img + (size_t)4 * (2 * R * 128);
     const bool done = __all_sync(0xffffffffu, ptx::mbar_wait(d_full, 0, nullptr));
     if (!done && lane == 0) latch(err, kErrTimeout, 9300000 + h);
     ptx::tc_fence_after();
     float amax = 0.f;
     if (warp_on) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(rope[i]));
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(rope[i]));
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
             uint32_t r[32];
             ptx::tmem_ld32(src_col + c, r);
             ptx::tmem_wait_ld();
@@ -945,18 +980,19 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
     s_max[cg * 128 + 32 * quad + lane] = amax;
     __syncthreads();
+    if (threadIdx.x < 128)
+        s_row[threadIdx.x] = fmaxf(fmaxf(s_max[threadIdx.x], s_max[128 + threadIdx.x]),
+                                   fmaxf(s_max[256 + threadIdx.x], s_max[384 + threadIdx.x]));
+    cluster_sync();
     if (warp_on) {
+        amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, s_max[i * 128 + 32 * quad + lane]);
+        for (int i = 0; i < kAbsorbCluster; ++i) amax = fmaxf(amax, ld_cluster(s_row + 32 * quad + lane, i));
         const int e = query_exponent(amax);
         // an infinite query value must not saturate: times 0 it is NaN, as its scores are
         const float inv = amax < INFINITY ? pow2i(-e) : 0.f;
-        const int R = s.R, b = v / s.q_len, t = v % s.q_len, row = t * s.H + h;
-        const size_t img = (size_t)2 * R * kRow, chunk = (size_t)2 * R * 128;
-        uint8_t* base = ws.q_img + ((size_t)b * s.G + row / R) * img;
-        const int rh = row % R, rl = R + rh;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
             uint32_t r[32];
             ptx::tmem_ld32(src_col + c, r);
             ptx::tmem_wait_ld();
@@ -965,42 +1001,45 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[16 * q + i]);
-                uint4 hi, lo;
-                split_e4m3(x, inv, hi, lo);
-                const int u = c / 16 + q;
+                uint32_t hi[4], lo[4];
+                split_e4m3<8>(x, inv, hi, lo);
+                const int u = 4 * (cg & 1) + c / 16 + q;   // 16-byte unit of the row's chunk
                 if (on) {
-                    *(uint4*)(base + cg * chunk + rh * 128 + ((u ^ (rh & 7)) << 4)) = hi;
-                    *(uint4*)(base + cg * chunk + rl * 128 + ((u ^ (rl & 7)) << 4)) = lo;
+                    *(uint4*)(chunk + rh * 128 + ((u ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *(uint4*)(chunk + rl * 128 + ((u ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
         }
         if (on) {
-            uint4 hi, lo;
-            split_e4m3(rope, inv, hi, lo);
-            uint8_t* rp = base + 4 * chunk;
-            *(uint4*)(rp + rh * 64 + ((cg ^ ((rh >> 1) & 3)) << 4)) = hi;
-            *(uint4*)(rp + rl * 64 + ((cg ^ ((rl >> 1) & 3)) << 4)) = lo;
-            if (cg == 0) ws.q_scale[((size_t)b * s.G + row / R) * R + rh] = pow2i(e);
+            uint32_t hi[2], lo[2];
+            split_e4m3<4>(rope, inv, hi, lo);
+            const int ru = 2 * rank + (cg >> 1);   // 16-byte unit of the rotary part
+            *(uint2*)(rp + rh * 64 + ((ru ^ ((rh >> 1) & 3)) << 4) + 8 * (cg & 1)) = make_uint2(hi[0], hi[1]);
+            *(uint2*)(rp + rl * 64 + ((ru ^ ((rl >> 1) & 3)) << 4) + 8 * (cg & 1)) = make_uint2(lo[0], lo[1]);
+            if (rank == 0 && cg == 0) ws.q_scale[item * R + rh] = pow2i(e);
             // rows that pad a sequence's last group are zero: head h writes the h-th, (h + H)-th, ...
             if (t == s.q_len - 1) {
+#pragma unroll 1
                 for (int p = s.q_len * s.H + h; p < s.G * R; p += s.H) {
                     const int ph = p % R, pl = R + ph;
                     uint8_t* pb = ws.q_img + ((size_t)b * s.G + p / R) * img;
+                    uint8_t* pc = pb + (size_t)(2 * rank + (cg >> 1)) * (2 * R * 128);
                     const uint4 z = make_uint4(0, 0, 0, 0);
-                    for (int u = 0; u < 8; ++u) {
-                        *(uint4*)(pb + cg * chunk + ph * 128 + 16 * u) = z;
-                        *(uint4*)(pb + cg * chunk + pl * 128 + 16 * u) = z;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        *(uint4*)(pc + ph * 128 + 64 * (cg & 1) + 16 * u) = z;
+                        *(uint4*)(pc + pl * 128 + 64 * (cg & 1) + 16 * u) = z;
                     }
-                    *(uint4*)(pb + 4 * chunk + ph * 64 + 16 * cg) = z;
-                    *(uint4*)(pb + 4 * chunk + pl * 64 + 16 * cg) = z;
-                    if (cg == 0) ws.q_scale[((size_t)b * s.G + p / R) * R + ph] = 1.f;
+                    *(uint2*)(pb + (size_t)4 * (2 * R * 128) + ph * 64 + 32 * rank + 8 * cg) = make_uint2(0, 0);
+                    *(uint2*)(pb + (size_t)4 * (2 * R * 128) + pl * 64 + 32 * rank + 8 * cg) = make_uint2(0, 0);
+                    if (rank == 0 && cg == 0) ws.q_scale[((size_t)b * s.G + p / R) * R + ph] = 1.f;
                 }
             }
         }
     }
     ptx::tc_fence_before();
-    __syncthreads();
-    if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+    cluster_sync();   // no CTA leaves while another reads its shared memory
+    if (warp == 1) ptx::tmem_dealloc(tmem, 256);
 }
 
 // ------------------------------------------------------------- merge and W_UV
@@ -1039,69 +1078,109 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         ptx::tmem_alloc(tmem_slot, kMergeN);
         ptx::tmem_relinquish();
     }
-    pdl_wait();   // the partials come from the attention kernel
-    const long long per = ws.plan[0];
-#pragma unroll 1
+    // More than 8 queries: rows warp and warp + 16, both rows' requests in flight together.
+    // Fewer: `shares` warps take every shares-th piece of one row each (a row of one long
+    // sequence has a piece per CTA).
+    const int rows = min(kMergeN, NV - n0);
+    const int shares = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16, share = warp % shares;
+    int item[2], rin[2];
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int r = warp + 16 * k, v = n0 + r;
+        const int v = min(n0 + (shares > 1 ? warp / shares : warp + 16 * k), NV - 1);
+        const int b = v / s.q_len, row = (v - b * s.q_len) * s.H + h, g = row / s.R;
+        item[k] = b * s.G + g;
+        rin[k] = row - g * s.R;
+    }
+    pdl_wait();   // the partials come from the attention kernel
+    int2 pc[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) pc[k] = ws.pieces[item[k]];
+    auto at = [&](int k, int p) -> size_t {   // row of part_o and part_ml
+        return (size_t)(p == 0 ? item[k] : pc[k].x + (p - 1) * s.sib) * s.R + rin[k];
+    };
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 ml[2];        // statistics of the first 32 pieces (lane p)
+    uint4 x[2][4][2];    // this warp's first four pieces
+    auto request = [&](int k, int i0) {   // pieces share + shares (i0 .. i0 + 3)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int p = min(share + shares * (i0 + q), max(pc[k].y - 1, 0));
+            const uint4* from = (const uint4*)(ws.part_o + at(k, p) * kDc + 16 * lane);
+            x[k][q][0] = from[0];
+            x[k][q][1] = from[1];
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        ml[k] = lane < pc[k].y ? ws.part_ml[at(k, lane)] : none;
+        request(k, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (shares > 1 && k > 0) break;
+        const int r = shares > 1 ? warp / shares : warp + 16 * k, np = pc[k].y;
         float acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-        if (v < NV) {
-            const int b = v / s.q_len, row = (v % s.q_len) * s.H + h, g = row / s.R, rin = row % s.R;
-            const long long item = (long long)b * s.G + g;
-            const int L = src.len(b), nt = tiles_of(src.keys(L, src.last_token(g)));
-            const long long t0 = ws.plan[1 + (s.sib > 1 ? b : item)] + kPieceCost, k0 = t0 / per;
-            const int np = nt > 0 ? (int)((t0 + nt - 1) / per - k0) + 1 : 0;
-            auto slot_row = [&](int p) -> size_t {
-                const long long slot = p == 0 ? item : (long long)s.B * s.G + (k0 + p) * s.sib + (s.sib > 1 ? g : 0);
-                return (size_t)slot * s.R + rin;
-            };
-            float M = -INFINITY;
-            for (int p = lane; p < np; p += 32) {
-                const float4 ml = ws.part_ml[slot_row(p)];
-                if (ml.y != 0.f) M = fmaxf(M, ml.x);   // a piece without a key of this row has no reference
-            }
+        // a piece without a key of this row (sum 0) has no reference
+        float M = ml[k].y != 0.f ? ml[k].x : -INFINITY;
+#pragma unroll 1
+        for (int p = 32 + lane; p < np; p += 32) {
+            const float4 o = ws.part_ml[at(k, p)];
+            if (o.y != 0.f) M = fmaxf(M, o.x);
+        }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float sum = 0.f;
-            for (int p0 = 0; p0 < np; p0 += 32) {
-                float w = 0.f;
-                if (p0 + lane < np) {
-                    const float4 ml = ws.part_ml[slot_row(p0 + lane)];
-                    const float x = ml.y != 0.f ? exp2f(ml.x - M) * ml.y : 0.f;
-                    sum += x;
-                    w = x * ml.z;
-                }
-                const int n = min(32, np - p0);
-                for (int q0 = 0; q0 < n; q0 += 4) {   // four pieces' rows in flight
-                    uint4 x[4][2];
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float sum = 0.f;
+#pragma unroll 1
+        for (int p0 = 0; p0 < np; p0 += 32) {   // lane i: weight of piece p0 + i
+            if (p0 > 0) ml[k] = p0 + lane < np ? ws.part_ml[at(k, p0 + lane)] : none;
+            const float e = ml[k].y != 0.f ? exp2f(ml[k].x - M) * ml[k].y : 0.f, w = e * ml[k].z;
+            sum += e;
+            const int n = min(32, np - p0);   // (shares divides 32)
+#pragma unroll 1
+            for (int q0 = share; q0 < n; q0 += 4 * shares) {
+                if (p0 + q0 > share) request(k, (p0 + q0) / shares);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4* from = (const uint4*)(ws.part_o + slot_row(p0 + min(q0 + q, n - 1)) * kDc + 16 * lane);
-                        x[q][0] = from[0];
-                        x[q][1] = from[1];
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const int i = q0 + q * shares;
+                    const float wq = __shfl_sync(0xffffffffu, w, i & 31);
+                    if (i < n && wq != 0.f) {
+                        const uint32_t word[8] = {x[k][q][0].x, x[k][q][0].y, x[k][q][0].z, x[k][q][0].w,
+                                                  x[k][q][1].x, x[k][q][1].y, x[k][q][1].z, x[k][q][1].w};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float wq = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
-                        if (q0 + q < n && wq != 0.f) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint32_t word = i < 4 ? (&x[q][0].x)[i] : (&x[q][1].x)[i - 4];
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word));
-                                acc[2 * i] = fmaf(wq, f.x, acc[2 * i]);
-                                acc[2 * i + 1] = fmaf(wq, f.y, acc[2 * i + 1]);
-                            }
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word[c]));
+                            acc[2 * c] = fmaf(wq, f.x, acc[2 * c]);
+                            acc[2 * c + 1] = fmaf(wq, f.y, acc[2 * c + 1]);
                         }
                     }
                 }
             }
+        }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] *= inv;
+        for (int i = 0; i < 16; ++i) acc[i] *= inv;
+        if (shares > 1) {   // the shares of a row meet in shared memory, and are added in order
+            float4* mine = (float4*)(sB + warp * 2048) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mine[32 * i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+            __syncthreads();
+            if (share == 0) {
+#pragma unroll 1
+                for (int o = 1; o < shares; ++o) {
+                    const float4* his = (const float4*)(sB + (warp + o) * 2048) + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = his[32 * i];
+                        acc[4 * i] += f.x, acc[4 * i + 1] += f.y, acc[4 * i + 2] += f.z, acc[4 * i + 3] += f.w;
+                    }
+                }
+            }
+            __syncthreads();   // the shares are read
+            if (share != 0) break;
         }
         // columns 16 lane .. +15 of row r: chunk lane / 4, 16-byte units 2 (lane % 4) and + 1
         uint32_t hi[8], lo[8];
@@ -1111,24 +1190,24 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
             lo[i] = ptx::pack_bf16(acc[2 * i] - __uint_as_float(hi[i] << 16),
                                    acc[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
         }
-        uint8_t* at = sB + (lane >> 2) * (kMergeN * 128) + r * 128;
+        uint8_t* to = sB + (lane >> 2) * (kMergeN * 128) + r * 128;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int u = ((2 * (lane & 3) + q) ^ (r & 7)) << 4;
-            *(uint4*)(at + u) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-            *(uint4*)(at + kMergeB + u) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+            *(uint4*)(to + u) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+            *(uint4*)(to + kMergeB + u) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
         }
     }
     ptx::fence_proxy_async_smem();   // read by the tensor cores
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    if (threadIdx.x == 32) {
-        if (!ptx::mbar_wait(a_full, 0, nullptr)) {
-            latch(err, kErrTimeout, 9400000 + h);
-        } else {
-            ptx::tc_fence_after();
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    if (warp == 1) {
+        const bool landed = ptx::mbar_wait(a_full, 0, nullptr);
+        if (!landed) latch(err, kErrTimeout, 9400000 + h);
+        ptx::tc_fence_after();
+        if (landed && elect()) {
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, kMergeN, 0, 0);
 #pragma unroll
             for (int term = 1; term >= 0; --term)
@@ -1140,7 +1219,7 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
                                     ptx::desc_kmajor_sw128(ptx::smem_u32(sB + term * kMergeB + kc * kMergeN * 128) + 32 * k),
                                     idesc, term == 0 || (kc | k) != 0);
         }
-        ptx::mma_commit(d_full);
+        if (elect()) ptx::mma_commit(d_full);
     }
     __syncwarp();
     if (warp < 4) {
@@ -1206,7 +1285,8 @@ Ws carve(char* base, const Shape& s) {
     w.q_scale = (float*)take(items * s.R * 4);
     w.part_o = (__half*)take(slots * s.R * kDc * 2);
     w.part_ml = (float4*)take(slots * s.R * 16);
-    w.plan = (long long*)take((items + 1) * 8);
+    w.start = (int4*)take((size_t)s.ctas * 16);
+    w.pieces = (int2*)take(items * 8);
     w.bytes = off;
     return w;
 }
@@ -1225,8 +1305,8 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
         if (!make_tmap_bf16(&mq, p.q_nope, 3, dq, sq, bq) || !make_tmap_bf16(&mk, p.W_UKT, 2, dw, sw, bw))
             return cudaErrorInvalidValue;
         if ((e = set_smem(absorb_kernel, kAbsorbSmem)) != cudaSuccess) return e;
-        e = launch_pdl(absorb_kernel, dim3(s.H, (unsigned)((NV + 127) / 128)), dim3(kAbsorbThreads), kAbsorbSmem, st, mq,
-                       mk, p.q_rope, s, ws, err);
+        e = launch_pdl(absorb_kernel, dim3(kAbsorbCluster * (s.H + 1), (unsigned)((NV + 127) / 128)),
+                       dim3(kAbsorbThreads), kAbsorbSmem, st, mq, mk, p.q_rope, src, ws, err);
         if (e != cudaSuccess) return e;
     }
     {

@@ -29,7 +29,8 @@ struct Ws {
     float* q_scale;     // [B G][R]
     __half* part_o;     // [slots][R][512] normalised partial outputs
     float4* part_ml;    // [slots][R] (reference, sum, scale of the output, -)
-    long long* plan;    // [1 + vseqs]: cost units per range, cost position of each virtual sequence
+    int4* start;        // [ctas]: where each range of the work split starts
+    int2* pieces;       // [B G]: slots and number of each item's partials
     size_t bytes;
 };
 
