@@ -123,6 +123,32 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) 
                  : "memory");
 }
 
+// Two fp32 values in one 64-bit register pair: one instruction for both
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(uint32_t x, uint32_t y) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ f32x2 pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ void unpair(f32x2 v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, pair(-1.f, -1.f), a); }
+
 __device__ __forceinline__ float ex2(float x) {   // flushes results below 2^-126
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -360,7 +386,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (ok && use > 0 && !wait_warp(&chunk_empty[slot], (use - 1) & 1, abort_flag)) ok = false;
-                    if (ok && elect()) {
+                    if (ok) if (elect()) {
                         uint8_t* dst = chunks + slot * kChunkBytes;
                         ptx::mbar_expect_tx(&chunk_full[slot], kChunkBytes);
                         ptx::tma_load_2d_hint(dst, &tm_lat, &chunk_full[slot], 128 * c, r0, policy);
@@ -504,7 +530,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             ++meets;
         };
         uint32_t piece = 0, g = 0;
-        float l[HC];               // this thread's share of each row's sum
+        f32x2 l[HC / 2];           // this thread's share of each row's sum
         float m_row = 0.f, m_top = 0.f;   // lane i: reference of row c0 + i, and the highest it has had
         while (ok && next_piece()) {
             float s_ref = 1.f, s_top = 0.f;
@@ -513,12 +539,24 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 const bool first = j == sg.j0;
                 if (first && !uwait(q_full, piece & 1)) { ok = false; break; }   // row scales
                 if (!uwait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }   // page scales
-                if (!uwait(&s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
                 // O of tile g - 2 is done (its P lay where this tile's goes); every phase of the
                 // barrier is waited for, so that a later wait cannot take an older one for its own
                 if (g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
+                float s = page_scale[2 * (g & 3) + (quad >> 1)];
+                if (first) {
+                    const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
+                    s_ref = sa != 0.f ? sa : sb != 0.f ? sb : 1.f;
+#pragma unroll
+                    for (int i = 0; i < HC / 2; ++i) l[i] = 0;
+                    m_row = 0.f;
+                }
+                s_top = fmaxf(s_top, s);
+                if (s == 0.f) s = s_ref;   // no page: zero rows
+                const bool same = s == s_ref;
+                const float kt = scale_log2 * s, shift = same ? 0.f : log2f(s) - log2f(s_ref), back = same ? 1.f : s_ref / s;
+                if (!uwait(&s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
                 ptx::tc_fence_after();
-                float arg[HC];
+                f32x2 arg[HC / 2];   // two rows each
                 {
                     uint32_t a[HC], b[HC];
                     tmem_ld(lane_addr + (g & 1) * (2 * R) + c0, a);
@@ -526,34 +564,19 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     ptx::tmem_wait_ld();
                     ptx::tc_fence_before();
 #pragma unroll
-                    for (int i = 0; i < HC; i += 4) {
-                        const float4 f = *(const float4*)(qs + c0 + i);
-                        arg[i] = (__uint_as_float(a[i]) + __uint_as_float(b[i])) * f.x;
-                        arg[i + 1] = (__uint_as_float(a[i + 1]) + __uint_as_float(b[i + 1])) * f.y;
-                        arg[i + 2] = (__uint_as_float(a[i + 2]) + __uint_as_float(b[i + 2])) * f.z;
-                        arg[i + 3] = (__uint_as_float(a[i + 3]) + __uint_as_float(b[i + 3])) * f.w;
+                    for (int i = 0; i < HC / 2; i += 2) {
+                        const ulonglong2 f = *(const ulonglong2*)(qs + c0 + 2 * i);
+                        arg[i] = mul2(add2(pair(a[2 * i], a[2 * i + 1]), pair(b[2 * i], b[2 * i + 1])), f.x);
+                        arg[i + 1] = mul2(add2(pair(a[2 * i + 2], a[2 * i + 3]), pair(b[2 * i + 2], b[2 * i + 3])), f.y);
                     }
                     ptx::mbar_arrive(&s_free[g & 1]);   // also done with the row scales
                 }
-                float s = page_scale[2 * (g & 3) + (quad >> 1)];
-                if (first) {
-                    const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
-                    s_ref = sa != 0.f ? sa : sb != 0.f ? sb : 1.f;
+                const f32x2 kt2 = pair(kt, kt), shift2 = pair(shift, shift);
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) l[i] = 0.f;
-                    m_row = 0.f;
-                }
-                s_top = fmaxf(s_top, s);
-                if (s == 0.f) s = s_ref;   // no page: zero rows
-                const bool same = s == s_ref;
-                const float kt = scale_log2 * s, shift = same ? 0.f : log2f(s) - log2f(s_ref), back = same ? 1.f : s_ref / s;
-#pragma unroll
-                for (int i = 0; i < HC; i += 4) {   // the first tile's arguments are set when its reference is
-                    const float4 m = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *(const float4*)(refs + grp * 16 + i);
-                    arg[i] = fmaf(arg[i], kt, shift - m.x);
-                    arg[i + 1] = fmaf(arg[i + 1], kt, shift - m.y);
-                    arg[i + 2] = fmaf(arg[i + 2], kt, shift - m.z);
-                    arg[i + 3] = fmaf(arg[i + 3], kt, shift - m.w);
+                for (int i = 0; i < HC / 2; i += 2) {   // the first tile's arguments are set when its reference is
+                    const ulonglong2 m = first ? make_ulonglong2(0, 0) : *(const ulonglong2*)(refs + grp * 16 + 2 * i);
+                    arg[i] = fma2(arg[i], kt2, sub2(shift2, m.x));
+                    arg[i + 1] = fma2(arg[i + 1], kt2, sub2(shift2, m.y));
                 }
                 const bool edge = (j + 1) * kT > sg.kmin;   // some row does not see the whole tile
                 if (edge) {
@@ -561,16 +584,21 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     if (sg.kmin == sg.kmax) {
                         if (at >= sg.kmax) {
 #pragma unroll
-                            for (int i = 0; i < HC; ++i) arg[i] = -INFINITY;
+                            for (int i = 0; i < HC / 2; ++i) arg[i] = pair(-INFINITY, -INFINITY);
                         }
                     } else {
                         const int row = sg.g * R + c0;
                         int t = row / src.s.H, h = row - t * src.s.H;   // of the thread's first row
                         int keys = src.keys(sg.len, t);
 #pragma unroll
-                        for (int i = 0; i < HC; ++i) {
-                            if (at >= keys) arg[i] = -INFINITY;
+                        for (int i = 0; i < HC / 2; ++i) {
+                            float x, y;
+                            unpair(arg[i], x, y);
+                            if (at >= keys) x = -INFINITY;
                             if (++h == src.s.H) h = 0, ++keys;
+                            if (at >= keys) y = -INFINITY;
+                            if (++h == src.s.H) h = 0, ++keys;
+                            arg[i] = pair(x, y);
                         }
                     }
                 }
@@ -581,9 +609,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     uint32_t low = 0;
                     float top = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) {
-                        low = __funnelshift_l(__float_as_uint(arg[i]), low, 1);
-                        top = fmaxf(top, arg[i]);
+                    for (int i = 0; i < HC / 2; ++i) {
+                        float x, y;
+                        unpair(arg[i], x, y);
+                        low = __funnelshift_l(__float_as_uint(x), low, 1);
+                        low = __funnelshift_l(__float_as_uint(y), low, 1);
+                        top = fmaxf(fmaxf(top, x), y);
                     }
                     low = __reduce_and_sync(0xffffffffu, low);
                     if (__any_sync(0xffffffffu, top > kTopLog2)) low = 0xffffffffu;
@@ -597,9 +628,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     // this warp's largest argument of each row, then the tile's, row i in lane i
                     float keep = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) {
-                        const float v = warp_max(arg[i]);
-                        if (lane == i) keep = v;
+                    for (int i = 0; i < HC / 2; ++i) {
+                        float x, y;
+                        unpair(arg[i], x, y);
+                        x = warp_max(x);
+                        y = warp_max(y);
+                        if (lane == 2 * i) keep = x;
+                        if (lane == 2 * i + 1) keep = y;
                     }
                     if (lane < HC) ((float*)(red + grp * 16 + lane))[quad] = keep;
                     meet();
@@ -619,12 +654,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     const float alpha = ex2(-step);
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) arg[i] -= __shfl_sync(0xffffffffu, step, i);
+                    for (int i = 0; i < HC / 2; ++i)
+                        arg[i] = sub2(arg[i], pair(__shfl_sync(0xffffffffu, step, 2 * i), __shfl_sync(0xffffffffu, step, 2 * i + 1)));
                     if (!first && __any_sync(0xffffffffu, step != 0.f)) {   // the same in the four warps
                         if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
                         ptx::tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < HC; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
+                        for (int i = 0; i < HC / 2; ++i)
+                            l[i] = mul2(l[i], pair(__shfl_sync(0xffffffffu, alpha, 2 * i), __shfl_sync(0xffffffffu, alpha, 2 * i + 1)));
 #pragma unroll 1
                         for (int c = 0; c < 4 * (C::NP / R); ++c) {
                             uint32_t r[HC];
@@ -641,20 +678,17 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 }
                 // P in two E4M3 terms; the sums take the unrounded p
                 uint32_t hi8[HC / 4], lo8[HC / 4];
+                const f32x2 back2 = pair(back, back);
 #pragma unroll
-                for (int i = 0; i < HC; i += 4) {
-                    uint32_t h[2], t[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float p0 = ex2(arg[i + 2 * q]), p1 = ex2(arg[i + 2 * q + 1]);
-                        l[i + 2 * q] = fmaf(p0, back, l[i + 2 * q]);
-                        l[i + 2 * q + 1] = fmaf(p1, back, l[i + 2 * q + 1]);
-                        const uint32_t v = ptx::pack_f16(p0, p1);
-                        h[q] = e4m3x2_f16(v);
-                        t[q] = e4m3x2_f16(hsub2(v, f16x2_of_e4m3(h[q])));
-                    }
-                    hi8[i / 4] = h[0] | (h[1] << 16);
-                    lo8[i / 4] = t[0] | (t[1] << 16);
+                for (int i = 0; i < HC / 2; ++i) {
+                    float x, y;
+                    unpair(arg[i], x, y);
+                    x = ex2(x);
+                    y = ex2(y);
+                    l[i] = fma2(pair(x, y), back2, l[i]);
+                    const uint32_t v = ptx::pack_f16(x, y), h = e4m3x2_f16(v), t = e4m3x2_f16(hsub2(v, f16x2_of_e4m3(h)));
+                    hi8[i / 2] = i % 2 ? __byte_perm(hi8[i / 2], h, 0x5410) : h;
+                    lo8[i / 2] = i % 2 ? __byte_perm(lo8[i / 2], t, 0x5410) : t;
                 }
                 // row tok of P: 64 bytes, 16-byte unit u at u ^ (tok / 2 % 4)
                 uint8_t* prow = ropes + (g % NR) * kRopeBytes + tok * 64;
@@ -696,6 +730,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             if (!ok) break;
             // ---- the piece's sums over all tokens, then its normalised output
             // after step o, a lane holds the sums over 32 / o lanes of the rows whose bits match its own
+            float ls[HC];
+#pragma unroll
+            for (int i = 0; i < HC / 2; ++i) unpair(l[i], ls[2 * i], ls[2 * i + 1]);
 #pragma unroll
             for (int w = HC / 2, o = 16; o > 0; o >>= 1, w = w > 0 ? w / 2 : 0) {
                 if (w > 0) {
@@ -703,11 +740,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < HC / 2; ++i)
                         if (i < w) {
-                            const float mine = up ? l[i + w] : l[i], give = up ? l[i] : l[i + w];
-                            l[i] = mine + __shfl_xor_sync(0xffffffffu, give, o);
+                            const float mine = up ? ls[i + w] : ls[i], give = up ? ls[i] : ls[i + w];
+                            ls[i] = mine + __shfl_xor_sync(0xffffffffu, give, o);
                         }
                 } else {
-                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+                    ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], o);
                 }
             }
             // row held by this lane: the lane bits from 16 down, as many as HC has
@@ -715,7 +752,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             float* sums = (float*)(red + grp * 16);   // [4 quarters][16]
             meet();   // red is read
             if (!ok) break;
-            sums[quad * 16 + my_row] = l[0];
+            sums[quad * 16 + my_row] = ls[0];
             if (lane == 0) out_scale[grp * 4 + quad] = s_top;
             meet();
             if (!ok) break;
