@@ -166,10 +166,19 @@ __device__ __forceinline__ uint32_t e4m3x2_f32(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t h2) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+// four fp16 values <-> four E4M3 codes
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
     return r;
+}
+__device__ __forceinline__ void f16x4(uint32_t codes, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(codes));
 }
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t code2) {
     uint32_t h;
@@ -680,15 +689,19 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 uint32_t hi8[HC / 4], lo8[HC / 4];
                 const f32x2 back2 = pair(back, back);
 #pragma unroll
-                for (int i = 0; i < HC / 2; ++i) {
-                    float x, y;
-                    unpair(arg[i], x, y);
-                    x = ex2(x);
-                    y = ex2(y);
-                    l[i] = fma2(pair(x, y), back2, l[i]);
-                    const uint32_t v = ptx::pack_f16(x, y), h = e4m3x2_f16(v), t = e4m3x2_f16(hsub2(v, f16x2_of_e4m3(h)));
-                    hi8[i / 2] = i % 2 ? __byte_perm(hi8[i / 2], h, 0x5410) : h;
-                    lo8[i / 2] = i % 2 ? __byte_perm(lo8[i / 2], t, 0x5410) : t;
+                for (int i = 0; i < HC / 4; ++i) {
+                    float x[4];
+                    unpair(arg[2 * i], x[0], x[1]);
+                    unpair(arg[2 * i + 1], x[2], x[3]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) x[q] = ex2(x[q]);
+                    l[2 * i] = fma2(pair(x[0], x[1]), back2, l[2 * i]);
+                    l[2 * i + 1] = fma2(pair(x[2], x[3]), back2, l[2 * i + 1]);
+                    const uint32_t v0 = ptx::pack_f16(x[0], x[1]), v1 = ptx::pack_f16(x[2], x[3]);
+                    uint32_t f0, f1;
+                    hi8[i] = e4m3x4(v0, v1);
+                    f16x4(hi8[i], f0, f1);
+                    lo8[i] = e4m3x4(hsub2(v0, f0), hsub2(v1, f1));
                 }
                 // row tok of P: 64 bytes, 16-byte unit u at u ^ (tok / 2 % 4)
                 uint8_t* prow = ropes + (g % NR) * kRopeBytes + tok * 64;
