@@ -28,6 +28,8 @@
 // probabilities: z' = z + log2(s_j / s_ref) with s_ref the piece's first page's scale.
 #include <math.h>
 
+#include <atomic>
+
 #include "decode_q8.cuh"
 #include "paged_plan.h"
 #include "tc_common.cuh"
@@ -1295,18 +1297,26 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     if (warp == 1) ptx::tmem_dealloc(tmem, kMergeN);
 }
 
+// Dynamic shared memory and the largest carve-out, once per kernel and device
 template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+cudaError_t set_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
 
 template <int R>
 cudaError_t launch_attn(const CUtensorMap& ml, const CUtensorMap& mr, const Src& src, const Problem& p, const Ws& ws,
                         DevErr err, cudaStream_t st) {
-    cudaError_t e = set_smem(attn_kernel<R>, Cfg<R>::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = set_smem(attn_kernel<R>, Cfg<R>::kSmem, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_kernel<R>, dim3(src.s.ctas), dim3(Cfg<R>::kThreads), Cfg<R>::kSmem, st, ml, mr, src, p.block_table,
                       p.scales, p.num_pages, p.scale * 1.4426950408889634f, ws, err);
@@ -1354,7 +1364,8 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
         const uint32_t bw[2] = {64, 256};
         if (!make_tmap_bf16(&mq, p.q_nope, 3, dq, sq, bq) || !make_tmap_bf16(&mk, p.W_UKT, 2, dw, sw, bw))
             return cudaErrorInvalidValue;
-        if ((e = set_smem(absorb_kernel, kAbsorbSmem)) != cudaSuccess) return e;
+        static std::atomic<uint64_t> done{0};
+        if ((e = set_smem(absorb_kernel, kAbsorbSmem, done)) != cudaSuccess) return e;
         e = launch_pdl(absorb_kernel, dim3(kAbsorbCluster * (s.H + 1), (unsigned)((NV + 127) / 128)),
                        dim3(kAbsorbThreads), kAbsorbSmem, st, mq, mk, p.q_rope, src, ws, err);
         if (e != cudaSuccess) return e;
@@ -1375,7 +1386,8 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
     const uint64_t dv[2] = {kDc, H * 128}, sv[1] = {kDc * 2};
     const uint32_t bv[2] = {64, 128};
     if (!make_tmap_bf16(&mv, p.W_UV, 2, dv, sv, bv)) return cudaErrorInvalidValue;
-    if ((e = set_smem(merge_kernel, kMergeSmem)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> done{0};
+    if ((e = set_smem(merge_kernel, kMergeSmem, done)) != cudaSuccess) return e;
     return launch_pdl(merge_kernel, dim3(s.H, (unsigned)((NV + kMergeN - 1) / kMergeN)), dim3(kMergeThreads), kMergeSmem,
                       st, mv, src, ws, p.out, err);
 }
