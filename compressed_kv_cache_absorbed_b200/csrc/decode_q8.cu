@@ -15,10 +15,18 @@
 //     O^T [4 x 128 latents x R] += codes^T [512 x 128] . P [128 x R]    (hi and lo)
 // so the codes are the A operand of both, K-major for the scores and MN-major for O, from the
 // one copy in shared memory; 64 rows' O takes 256 TMEM columns, two score buffers the other
-// 256, and a CTA needs no other CTA's scores.  A thread of the softmax holds one token and R/2
-// rows: P goes to shared memory in the layout the product reads, sums stay per thread until
-// the end of a piece, and the only thing the token lanes must agree on is each row's
-// reference M (below).
+// 256, and a CTA needs no other CTA's scores.  A thread of the softmax holds one token and 16
+// rows (8 for R = 16): P goes to shared memory in the layout the product reads, sums stay per
+// thread until the end of a piece, and the only thing the token lanes must agree on is each
+// row's reference M (below).
+//
+// What bounds it.  R = 64: a tile is 18 score products of N = 128 (65 cycles each) and 32 O
+// products of N = 64 (48.5: the A operand's 4 KB from shared memory, not the arithmetic), 2770
+// cycles together; it takes ~3700, because scores of tile g + 2 need the slots that O of tile g
+// frees and their own loads (two tiles fit beside the queries), then 2300 cycles of softmax: a
+// loop of 7400 cycles over two tiles.  Measured, 128 heads, 32 sequences of 4096 tokens: 48.2 us
+// (82.4 k cycles, tensor pipe 49 % of them, 80 MB from DRAM); 16 heads, 48 ragged sequences of
+// 4500 tokens on average: 29.5 us, 119 MB, 62 % of a copy's bandwidth, the rest start and end.
 //
 // The reference.  p = 2^(z' - M) must fit E4M3 (<= 448) and must not sink into its subnormals
 // (step 2^-9), so M follows the scores in both directions: it is set so that the tile's
@@ -43,15 +51,25 @@ constexpr int kDc = 512, kDr = 64, kRow = 576;
 constexpr int kT = 128;                       // tokens per tile
 constexpr int kChunkBytes = kT * 128;         // 128 latent columns of a tile (128-byte swizzle)
 constexpr int kRopeBytes = kT * kDr;          // the rotary columns of a tile (64-byte swizzle)
-constexpr int kRoleThreads = 128;             // TMA warp, score issuer, O issuer, a warp without a role
-constexpr int kPieceCost = 1;                 // cost units of a piece's query load and epilogue, in tiles
+constexpr int kRoleThreads = 128;             // TMA warp, score issuer, O issuer, the warp that finds the pieces
+// Cost units of a piece's query load and epilogue, in tiles: 1.  With 2, which is nearer to what
+// a switch takes, the longest ranges are as long and the step no faster (128 heads, 32 x 4096:
+// 66.2 and 66.5 us; 100-token chunks: 141.2 and 143.8; ragged long contexts: 321 and 320).
+constexpr int kPieceCost = 1;
+// Up to this many groups of a sequence are walked side by side, so that its pages come from HBM
+// once and from L2 for the others.  Side by side and one after another: 2 groups 66.2 and 67.6
+// us, 64 ragged sequences of up to 32768 tokens 321 and 349; 8 groups 106.4 and 106.9; 10 groups
+// 133.9 and 132.2, where 148 CTAs no longer divide well by the groups.
 constexpr int kMaxSib = 8;
 constexpr float kTopLog2 = 8.5f;              // p <= 2^8.5
 constexpr float kSetLog2 = 5.f;               // a new reference puts the tile's largest p here
 constexpr float kFarLog2 = 64.f;              // how far below its highest value a reference may go
 
-// Shared memory: NC chunk slots, NR slots that hold a tile's rotary columns and then its P
-// (hi and, for R <= 32, lo), P's lo term (R = 64), the group's queries.
+// Shared memory: NC chunk slots (as many as fit), NR slots that hold a tile's rotary columns and
+// then its P (hi and, for R <= 32, lo), P's lo term (R = 64), the group's queries.  (Slots of their
+// own for the rotary columns, free once the scores are made, changed nothing; nor did bringing
+// the pages into L2 two tiles ahead: 321 -> 320 us on ragged long contexts, 51 -> 54 us with 16
+// heads.)
 // Softmax warps: four (one per 32 tokens) for each of CG groups of HC rows; 16 rows a thread
 // keep its scores, sums and references in registers beside four warps per scheduler.
 template <int R> struct Cfg {
@@ -257,7 +275,7 @@ struct SegIter {
     }
 };
 
-// A bounded wait of a whole warp, in few instructions (the kernel has some thirty of them)
+// A bounded wait of a whole warp, in few instructions (there are some thirty of them)
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
     uint32_t left = ptx::g_wait_limit;
 #pragma unroll 1
@@ -1324,6 +1342,9 @@ cudaError_t launch_attn(const CUtensorMap& ml, const CUtensorMap& mr, const Src&
 
 }  // namespace
 
+// Rows per group: the smallest of 16, 32 and 64 that holds a sequence's rows, else 64 (the most
+// whose O and scores fit the tensor memory).  Against 64 for all: 16 heads 46.0 and 61.2 us, 32
+// heads 49.4 and 57.3 us (48 ragged sequences of up to 9001 tokens).
 Shape make_shape(int B, int q_len, int H, int num_sms) {
     const int rows = q_len * H;
     Shape s{B, q_len, H, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 1, 1, num_sms};

@@ -434,6 +434,117 @@ def test_refused_tensors():
     assert mla.mla_get_device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("H,Q,B", [(16, 1, 1100), (128, 20, 30), (128, 9, 3), (5, 3, 600)])
+def test_more_sequences_or_groups_than_threads(H, Q, B):
+    """The work split past one round of the planner, and groups walked one after another."""
+    lens = [(37 * i) % 210 for i in range(B)]
+    Decode(H, Q, lens, seed=51).check(f"H={H} q_len={Q} B={B}")
+
+
+def test_sequences_that_share_pages():
+    D = Decode(64, 1, [300, 300, 140], seed=52)
+    D.table[1, :4] = D.table[0, :4]                      # a common prefix of 256 tokens
+    D.table[2, :2] = D.table[0, :2]
+    D.table[2, 2] = D.table[2, 1]                        # and the same page twice
+    D.check("shared pages")
+
+
+def test_nan_in_a_later_tokens_row_does_not_reach_an_earlier_token():
+    for H, Q in ((16, 3), (128, 2)):
+        D = Decode(H, Q, [200, 66], seed=53)
+        want = D.run()
+        for b, n in enumerate([200, 66]):                # the last new token's row
+            D.codes[int(D.table[b, (n - 1) // PAGE]), (n - 1) % PAGE, 3] = 0xFF
+        out = D.run()
+        assert mla.mla_get_device_error() == (0, 0)
+        assert torch.equal(out[:, :-1], want[:, :-1])
+        assert torch.isnan(out[:, -1]).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_bad_query_value_stays_in_its_row(bad):
+    D = Decode(20, 2, [300, 70], seed=54)
+    want = D.run()
+    D.qn[1, 0, 7, 5] = bad
+    D.qr[0, 1, 19, 63] = bad
+    out = D.run()
+    assert mla.mla_get_device_error() == (0, 0)
+    hit = torch.zeros(2, 2, 20, dtype=torch.bool, device=DEV)
+    hit[1, 0, 7] = hit[0, 1, 19] = True
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("gain", [0.0, 1e-20, 1e-3, 30.0, 1e4])
+def test_query_sizes(gain):
+    """Rows of very different size in one group: each has its own scale."""
+    D = Decode(64, 1, [400, 129], seed=55)
+    D.qn[:, :, ::3] *= gain
+    D.qr[:, :, ::3] *= gain
+    if gain <= 1.0:
+        D.check(f"gain {gain}")
+        return
+    # huge scores: the softmax is nearly one-hot, and an output differs by the error of the
+    # scores' difference of its first two keys; only the rows of ordinary size are compared
+    got, want = D.run(), D.plain()
+    assert mla.mla_get_device_error() == (0, 0) and torch.isfinite(got.float()).all()
+    keep = torch.arange(64, device=DEV) % 3 != 0
+    assert_close(got[:, :, keep].float(), want[:, :, keep], "bf16", f"gain {gain}, other rows")
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    Ds = [Decode(128, 1, [3000, 10, 400], seed=56), Decode(16, 4, [900] * 5, seed=57)]
+    want = [D.run() for D in Ds]
+    streams = [torch.cuda.Stream() for _ in Ds]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for D, s, o in zip(Ds, streams, outs):
+            with torch.cuda.stream(s):
+                D.run(out=o)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == (0, 0)
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_empty_calls_are_no_ops():
+    D = Decode(16, 1, [5], seed=58)
+    none = lambda *s, t=torch.bfloat16: torch.empty(*s, dtype=t, device=DEV)  # noqa: E731
+    mla.mla_decode_absorbed_paged_q8(D.d, D.w, D.codes, D.scales, none(0, 3, t=torch.int32), none(0, t=torch.int32),
+                                     none(0, 1, 16, 128), D.ws, none(0, 1, 16, 128), none(0, 1, 16, 64))
+    codes, scales = D.codes.clone(), D.scales.clone()
+    mla.mla_append_paged_q8(D.d, none(0, DC), none(0, DR), i32([0, 0]), i32([5]), D.codes, D.scales, D.table)
+    cache = torch.ones(2, PAGE, ROW, dtype=torch.bfloat16, device=DEV)
+    mla.mla_append_paged(D.d, none(0, DC), none(0, DR), i32([0, 0]), i32([5]), cache, D.table)
+    assert torch.equal(D.codes, codes) and torch.equal(D.scales, scales) and (cache == 1).all()
+    out = Decode(16, 2, [0, 0], seed=59).run()
+    assert (out == 0).all() and mla.mla_get_device_error() == (0, 0)
+
+
+def test_appends_captured_and_replayed():
+    """A step's append in a graph, replayed with new rows and lengths in the same buffers."""
+    B, steps = 5, 70
+    g = gen(60)
+    c, k = torch.empty(B, DC, dtype=torch.bfloat16, device=DEV), torch.empty(B, DR, dtype=torch.bfloat16, device=DEV)
+    off, lens = i32(list(range(B + 1))), i32([1, 60, 64, 128, 3])
+    table, pages = page_table([n + steps for n in lens.tolist()], g)
+    codes = torch.zeros(pages, PAGE, ROW, dtype=torch.uint8, device=DEV)
+    scales = torch.ones(pages, device=DEV)
+    same, same_s = codes.clone(), scales.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        mla.mla_append_paged_q8(dims(), c, k, off, lens, codes, scales, table)
+    for step in range(steps):
+        c.copy_(torch.randn(B, DC, generator=g, device=DEV) * (1 + step % 7))
+        k.copy_(torch.randn(B, DR, generator=g, device=DEV))
+        graph.replay()
+        mla.mla_append_paged_q8(dims(), c, k, off, lens, same, same_s, table)
+        lens += 1
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == (0, 0)
+    assert torch.equal(codes, same) and torch.equal(scales, same_s)
+
+
 # ----------------------------------------------------------------- the run of them
 
 def test_prefill_append_steps_and_decode_together():
