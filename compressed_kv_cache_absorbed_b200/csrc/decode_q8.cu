@@ -966,7 +966,7 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     extern __shared__ uint8_t absorb_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)absorb_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + kAbsorbA;
-    float* s_max = (float*)(sB + kAbsorbB);   // [4 column groups][128]
+    float* s_max = (float*)(sB + kAbsorbB);   // [512] each thread's
     float* s_row = s_max + 512;               // [128] this CTA's largest value of each query
     uint64_t* full = (uint64_t*)(s_row + 128);
     uint64_t* d_full = full + 1;
@@ -974,6 +974,9 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int h = blockIdx.x / kAbsorbCluster, rank = blockIdx.x % kAbsorbCluster;
     const int v0 = blockIdx.y * 128, NV = s.B * s.q_len;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, cg = warp >> 2;
+    // With 64 queries or fewer, the lane quarters hold them twice or four times over, and each
+    // copy's warps convert a share of the columns: 16 warps at work instead of 4 on a step of 32.
+    const int blocks = NV - v0 <= 32 ? 1 : NV - v0 <= 64 ? 2 : 4, share = quad / blocks, width = 16 * blocks;
     if (threadIdx.x == 0) {
         ptx::mbar_init(full, 1);
         ptx::mbar_init(d_full, 1);
@@ -985,7 +988,10 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         pdl_wait();      // all earlier work is done
         pdl_trigger();   // only now may the next kernel launch
 #pragma unroll
-        for (int kc = 0; kc < 2; ++kc) ptx::tma_load_3d(sA + kc * 16384, &tm_q, full, 64 * kc, v0, h);
+        for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ptx::tma_load_3d(sA + kc * 16384 + i * 4096, &tm_q, full, 64 * kc, v0 + 32 * (i % blocks), h);
     }
     if (warp == 1) {
         ptx::tmem_alloc(tmem_slot, 256);
@@ -1012,9 +1018,10 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         __syncwarp();
     }
-    const int v = v0 + 32 * quad + lane;
-    const bool warp_on = v0 + 32 * quad < NV, on = v < NV;
-    const uint32_t src_col = tmem + ((uint32_t)(32 * quad) << 16) + 64 * cg;
+    const int v = v0 + 32 * (quad % blocks) + lane;
+    const bool warp_on = v0 + 32 * (quad % blocks) < NV, on = v < NV;
+    const int c0 = 64 * cg + width * share;   // this warp's columns: width from c0
+    const uint32_t src_col = tmem + ((uint32_t)(32 * quad) << 16) + c0;
     // this warp's 8 rotary columns; they may come from the previous kernel
     pdl_wait();
     float rope[8] = {};
@@ -1040,47 +1047,48 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(rope[i]));
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-            uint32_t r[32];
-            ptx::tmem_ld32(src_col + c, r);
+        for (int c = 0; c < width; c += 16) {
+            uint32_t r[16];
+            tmem_ld(src_col + c, r);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(r[i])));
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(__uint_as_float(r[i])));
         }
     }
-    s_max[cg * 128 + 32 * quad + lane] = amax;
+    s_max[threadIdx.x] = amax;
     __syncthreads();
-    if (threadIdx.x < 128)
-        s_row[threadIdx.x] = fmaxf(fmaxf(s_max[threadIdx.x], s_max[128 + threadIdx.x]),
-                                   fmaxf(s_max[256 + threadIdx.x], s_max[384 + threadIdx.x]));
+    if (threadIdx.x < 128) {   // query threadIdx.x of the CTA: the warps that hold a part of it
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((i & 3) % blocks == (int)(threadIdx.x >> 5) % blocks) m = fmaxf(m, s_max[32 * i + lane]);
+        s_row[threadIdx.x] = m;
+    }
     cluster_sync();
     if (warp_on) {
         amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < kAbsorbCluster; ++i) amax = fmaxf(amax, ld_cluster(s_row + 32 * quad + lane, i));
+        for (int i = 0; i < kAbsorbCluster; ++i) amax = fmaxf(amax, ld_cluster(s_row + 32 * (quad % blocks) + lane, i));
         const int e = query_exponent(amax);
         // an infinite query value must not saturate: times 0 it is NaN, as its scores are
         const float inv = amax < INFINITY ? pow2i(-e) : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-            uint32_t r[32];
-            ptx::tmem_ld32(src_col + c, r);
+        for (int c = 0; c < width; c += 16) {
+            uint32_t r[16];
+            tmem_ld(src_col + c, r);
             ptx::tmem_wait_ld();
+            float x[16];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float x[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[16 * q + i]);
-                uint32_t hi[4], lo[4];
-                split_e4m3<8>(x, inv, hi, lo);
-                const int u = 4 * (cg & 1) + c / 16 + q;   // 16-byte unit of the row's chunk
-                if (on) {
-                    *(uint4*)(chunk + rh * 128 + ((u ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *(uint4*)(chunk + rl * 128 + ((u ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
+            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+            uint32_t hi[4], lo[4];
+            split_e4m3<8>(x, inv, hi, lo);
+            const int u = (c0 + c) / 16 & 7;   // 16-byte unit of the row's chunk
+            if (on) {
+                *(uint4*)(chunk + rh * 128 + ((u ^ (rh & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4*)(chunk + rl * 128 + ((u ^ (rl & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
-        if (on) {
+        if (on && share == 0) {
             uint32_t hi[2], lo[2];
             split_e4m3<4>(rope, inv, hi, lo);
             const int ru = 2 * rank + (cg >> 1);   // 16-byte unit of the rotary part
@@ -1279,9 +1287,9 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         ptx::tc_fence_after();
         if (landed && elect()) {
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, kMergeN, 0, 0);
-#pragma unroll
+#pragma unroll 1
             for (int term = 1; term >= 0; --term)
-#pragma unroll
+#pragma unroll 1
                 for (int kc = 0; kc < 8; ++kc)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -1380,7 +1388,7 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
     {
         ProfScope ps(st, "q8_absorb");
         const uint64_t dq[3] = {128, NV, H}, sq[2] = {H * 256, 256};
-        const uint32_t bq[3] = {64, 128, 1};
+        const uint32_t bq[3] = {64, 32, 1};
         const uint64_t dw[2] = {128, H * kDc}, sw[1] = {256};
         const uint32_t bw[2] = {64, 256};
         if (!make_tmap_bf16(&mq, p.q_nope, 3, dq, sq, bq) || !make_tmap_bf16(&mk, p.W_UKT, 2, dw, sw, bw))
