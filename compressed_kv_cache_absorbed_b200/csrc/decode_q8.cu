@@ -83,7 +83,7 @@ template <int R> struct Cfg {
     static constexpr int kQBytes = 2 * R * kRow;
     static constexpr uint32_t kColO = 4 * R;
     static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
-    static constexpr int kMisc = 3072;
+    static constexpr int kMisc = 3 * 1024;
     static constexpr int kSmem = NC * kChunkBytes + NR * kRopeBytes + kLoBytes + kQBytes + kMisc;
     static_assert(kColO + 4 * NP <= kTmemCols, "TMEM columns");
     static_assert(kSmem <= 232448, "shared memory over the 227 KB limit");
