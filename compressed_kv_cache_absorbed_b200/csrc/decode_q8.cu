@@ -309,8 +309,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     uint8_t* qimg = plo + C::kLoBytes;
     float* qs = (float*)(qimg + C::kQBytes);            // [R] row scales of the queries
     float4* red = (float4*)(qs + 64);                   // [CG][16] per row, one value per token quarter
-    float* refs = (float*)(red + 64);                   // [CG][16] each row's reference
-    uint64_t* bars = (uint64_t*)(refs + 64);
+    float* nrefs = (float*)(red + 64);                  // [R] each row's reference, negated
+    float* row_kt = nrefs + 64;                         // [R] row scale x softmax scale x the piece's first page's scale
+    uint64_t* bars = (uint64_t*)(row_kt + 64);
     uint64_t *chunk_full = bars, *chunk_empty = bars + NC, *rope_full = bars + 2 * NC, *rope_empty = rope_full + 2;
     uint64_t *q_full = rope_full + 4, *s_full = rope_full + 5, *s_free = rope_full + 7, *p_ready = rope_full + 9;
     uint64_t *o_done = rope_full + 12, *grp_bar = rope_full + 14, *drain = rope_full + 18;
@@ -321,7 +322,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     float* out_scale = page_scale + 8;                  // [CG][4] largest page scale a warp saw
     uint32_t* tmem_slot = (uint32_t*)(out_scale + 16);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-    static_assert(64 * 4 + 64 * 16 + 64 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
+    static_assert(64 * 4 + 64 * 16 + 128 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
     static_assert(NC % 2 == 0, "16-byte alignment of the words behind the barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -568,9 +569,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 const bool first = j == sg.j0;
                 if (first && !uwait(q_full, piece & 1)) { ok = false; break; }   // row scales
                 if (!uwait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }   // page scales
-                // O of tile g - 2 is done (its P lay where this tile's goes); every phase of the
-                // barrier is waited for, so that a later wait cannot take an older one for its own
-                if (g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
+                // O of tile g - 2 is done, whose P lay where this tile's goes (R = 64 waits for tile
+                // g - 1 below).  Every phase of a barrier is waited for, so that a later wait cannot
+                // take an older one for its own.
+                if (!C::kTwoPass && g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
                 float s = page_scale[2 * (g & 3) + (quad >> 1)];
                 if (first) {
                     const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
@@ -578,11 +580,16 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < HC / 2; ++i) l[i] = 0;
                     m_row = 0.f;
+                    if (lane < HC) {   // the four warps write the same; read by a warp that wrote
+                        nrefs[c0 + lane] = 0.f;
+                        row_kt[c0 + lane] = qs[c0 + lane] * (scale_log2 * s_ref);
+                    }
+                    __syncwarp();
                 }
                 s_top = fmaxf(s_top, s);
                 if (s == 0.f) s = s_ref;   // no page: zero rows
                 const bool same = s == s_ref;
-                const float kt = scale_log2 * s, shift = same ? 0.f : log2f(s) - log2f(s_ref), back = same ? 1.f : s_ref / s;
+                const float back = same ? 1.f : s_ref / s;
                 if (!uwait(&s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
                 ptx::tc_fence_after();
                 f32x2 arg[HC / 2];   // two rows each
@@ -593,20 +600,25 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     ptx::tmem_wait_ld();
                     ptx::tc_fence_before();
 #pragma unroll
-                    for (int i = 0; i < HC / 2; i += 2) {
-                        const ulonglong2 f = *(const ulonglong2*)(qs + c0 + 2 * i);
-                        arg[i] = mul2(add2(pair(a[2 * i], a[2 * i + 1]), pair(b[2 * i], b[2 * i + 1])), f.x);
-                        arg[i + 1] = mul2(add2(pair(a[2 * i + 2], a[2 * i + 3]), pair(b[2 * i + 2], b[2 * i + 3])), f.y);
-                    }
-                    ptx::mbar_arrive(&s_free[g & 1]);   // also done with the row scales
+                    for (int i = 0; i < HC / 2; ++i) arg[i] = add2(pair(a[2 * i], a[2 * i + 1]), pair(b[2 * i], b[2 * i + 1]));
                 }
-                const f32x2 kt2 = pair(kt, kt), shift2 = pair(shift, shift);
+                if (same) {
 #pragma unroll
-                for (int i = 0; i < HC / 2; i += 2) {   // the first tile's arguments are set when its reference is
-                    const ulonglong2 m = first ? make_ulonglong2(0, 0) : *(const ulonglong2*)(refs + grp * 16 + 2 * i);
-                    arg[i] = fma2(arg[i], kt2, sub2(shift2, m.x));
-                    arg[i + 1] = fma2(arg[i + 1], kt2, sub2(shift2, m.y));
+                    for (int i = 0; i < HC / 2; i += 2) {
+                        const ulonglong2 f = *(const ulonglong2*)(row_kt + c0 + 2 * i), m = *(const ulonglong2*)(nrefs + c0 + 2 * i);
+                        arg[i] = fma2(arg[i], f.x, m.x);
+                        arg[i + 1] = fma2(arg[i + 1], f.y, m.y);
+                    }
+                } else {   // a page of another scale than the piece's first
+                    const float kt = scale_log2 * s, shift = log2f(s) - log2f(s_ref);
+#pragma unroll
+                    for (int i = 0; i < HC / 2; i += 2) {
+                        const ulonglong2 f = *(const ulonglong2*)(qs + c0 + 2 * i), m = *(const ulonglong2*)(nrefs + c0 + 2 * i);
+                        arg[i] = fma2(arg[i], mul2(f.x, pair(kt, kt)), add2(m.x, pair(shift, shift)));
+                        arg[i + 1] = fma2(arg[i + 1], mul2(f.y, pair(kt, kt)), add2(m.y, pair(shift, shift)));
+                    }
                 }
+                ptx::mbar_arrive(&s_free[g & 1]);   // also done with the row scales
                 const bool edge = (j + 1) * kT > sg.kmin;   // some row does not see the whole tile
                 if (edge) {
                     const int at = j * kT + tok;
@@ -678,7 +690,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                         }
                         m_row += step;
                         m_top = first ? m_row : fmaxf(m_top, m_row);
-                        refs[grp * 16 + lane] = m_row;   // the four warps write the same
+                        nrefs[c0 + lane] = -m_row;   // the four warps write the same
                     }
                     const float alpha = ex2(-step);
                     __syncwarp();
