@@ -280,78 +280,72 @@ def mla_decode_absorbed_fp8(dims, weights: MLAWeights, cache_fp8, offsets, out, 
 
 # The paged-cache calls below check what the C ABI cannot see behind a pointer (types, shapes,
 # strides, devices) and run on the tensors' own device, whichever is current.  A step makes
-# them once per layer, so the checks are few comparisons and say what is wrong only when
-# something is.
+# them once per layer and an append's kernel is shorter than its call, so the checks are few
+# comparisons, made in place, and say what is wrong only when something is.
 
-def _refuse(t, name, dtype, shape, device):
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_raw_stream, _swap_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_maybeExchangeDevice
+
+
+def _refuse(t, name, dtype, shape, dev):
     if t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, not {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: on {t.device}, not {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not cuda:{dev}")
     raise ValueError(f"{name}: not contiguous (strides {t.stride()})")
 
 
-def _tensor(t, name: str, dtype, shape, device) -> int:
-    """Device pointer of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
-        _refuse(t, name, dtype, shape, device)
+def _tensor(t, name: str, dtype, shape, dev: int) -> int:
+    """Device pointer of a contiguous tensor of this type, shape and CUDA device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _rows(t, name: str, dtype, n: int, width: int, device):
-    """(pointer, row stride in elements) of an [n, width] tensor with contiguous rows."""
-    if t.dtype != dtype or t.shape != (n, width) or t.device != device or not t.is_cuda:
-        _refuse(t, name, dtype, (n, width), device)
-    if n == 0:
-        return t.data_ptr(), width
+def _rows(t, name: str, dtype, n: int, width: int, dev: int) -> int:
+    """Row stride in elements of an [n, width] tensor with contiguous rows."""
+    if t.dtype is not dtype or t.shape != (n, width) or t.get_device() != dev:
+        _refuse(t, name, dtype, (n, width), dev)
     ld, step = t.stride()
-    if step != 1:
-        raise ValueError(f"{name}: columns are not contiguous (strides {t.stride()})")
-    if n == 1:
+    if n <= 1:
         ld = width
-    elif ld < width:
-        raise ValueError(f"{name}: rows overlap (stride {ld}, width {width})")
-    return t.data_ptr(), ld
+    if (step != 1 and n > 0) or ld < width:
+        raise ValueError(f"{name}: columns not contiguous, or rows that overlap (strides {t.stride()}, width {width})")
+    return ld
 
 
-class _on_device:
-    """Makes a device current while a call is made, if it is not; and finds the stream."""
-    __slots__ = ("ctx", "raw")
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"tensors on {device}, not a CUDA device")
-        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.raw = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-
-def _append_paged(call, name, dims, c, k_r, new_offsets, seq_lens, pages, scales, block_table, pos, stream):
-    dev, i32 = pages[0].device, torch.int32
-    st = torch.bfloat16 if dims.dtype == MLA_BF16 else torch.float32
-    n, B = c.shape[0], seq_lens.numel()
-    cp, ld_c = _rows(c, "c", st, n, dims.d_c, dev)
-    kp, ld_k = _rows(k_r, "k_r", st, n, dims.d_hR, dev)
-    num_pages = pages[0].shape[0]
-    pg = _tensor(pages[0], pages[1], pages[2], (num_pages, 64, dims.d_c + dims.d_hR), dev)
-    off = _tensor(new_offsets, "new_offsets", i32, (B + 1,), dev)
-    lens = _tensor(seq_lens, "seq_lens", i32, (B,), dev)
-    bt = _tensor(block_table, "block_table", i32, (B, block_table.shape[-1]), dev)
-    pp = None if pos is None else _tensor(pos, "pos", i32, (n,), dev)
-    extra = () if scales is None else (_tensor(scales, "scales", torch.float32, (num_pages,), dev),)
-    with _on_device(dev, stream) as raw:
-        _check(call(ctypes.byref(dims), cp, ld_c, kp, ld_k, off, lens, pp, B, n, pg, *extra, num_pages, bt,
-                    block_table.shape[1], raw), name)
+def _append_paged(call, where, dims, c, k_r, new_offsets, seq_lens, pages, pages_name, pages_type, scales,
+                  block_table, pos, stream):
+    dev = pages.get_device()
+    if dev < 0:
+        raise ValueError(f"{pages_name}: on {pages.device}, not a CUDA device")
+    st = _BF16 if dims.dtype == MLA_BF16 else _F32
+    d_c, d_hR = dims.d_c, dims.d_hR
+    n, B, num_pages, max_blocks = len(c), seq_lens.numel(), len(pages), block_table.shape[-1]
+    ld_c = _rows(c, "c", st, n, d_c, dev)
+    ld_k = _rows(k_r, "k_r", st, n, d_hR, dev)
+    pg = _tensor(pages, pages_name, pages_type, (num_pages, 64, d_c + d_hR), dev)
+    off = _tensor(new_offsets, "new_offsets", _I32, (B + 1,), dev)
+    lens = _tensor(seq_lens, "seq_lens", _I32, (B,), dev)
+    bt = _tensor(block_table, "block_table", _I32, (B, max_blocks), dev)
+    pp = None if pos is None else _tensor(pos, "pos", _I32, (n,), dev)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    before = _swap_device(dev)
+    try:
+        if scales is None:
+            status = call(ctypes.byref(dims), c.data_ptr(), ld_c, k_r.data_ptr(), ld_k, off, lens, pp, B, n, pg,
+                          num_pages, bt, max_blocks, raw)
+        else:
+            sc = _tensor(scales, "scales", _F32, (num_pages,), dev)
+            status = call(ctypes.byref(dims), c.data_ptr(), ld_c, k_r.data_ptr(), ld_k, off, lens, pp, B, n, pg, sc,
+                          num_pages, bt, max_blocks, raw)
+    finally:
+        if before != dev:
+            _swap_device(before)
+    if status:
+        _check(status, where)
 
 
 def mla_append_paged(dims, c, k_r, new_offsets, seq_lens, cache_pages, block_table, pos=None, stream=None) -> None:
@@ -360,17 +354,16 @@ def mla_append_paged(dims, c, k_r, new_offsets, seq_lens, cache_pages, block_tab
     new_offsets[b] .. new_offsets[b+1] - 1 (int32 [B+1]) and the last of its seq_lens[b] tokens
     (int32 [B], after the append); block_table int32 [B, max_blocks]; pos int32 [n] or the
     tokens' places in their sequences."""
-    st = torch.bfloat16 if dims.dtype == MLA_BF16 else torch.float32
-    _append_paged(_lib.mla_append_paged, "mla_append_paged", dims, c, k_r, new_offsets, seq_lens,
-                  (cache_pages, "cache_pages", st), None, block_table, pos, stream)
+    _append_paged(_lib.mla_append_paged, "mla_append_paged", dims, c, k_r, new_offsets, seq_lens, cache_pages,
+                  "cache_pages", _BF16 if dims.dtype == MLA_BF16 else _F32, None, block_table, pos, stream)
 
 
 def mla_append_paged_q8(dims, c, k_r, new_offsets, seq_lens, codes, scales, block_table, pos=None,
                         stream=None) -> None:
     """mla_append_paged into an 8-bit cache: codes uint8 [num_pages, 64, 576] (FP8 E4M3), scales
     float32 [num_pages], one power of two per page (value = code * scale)."""
-    _append_paged(_lib.mla_append_paged_q8, "mla_append_paged_q8", dims, c, k_r, new_offsets, seq_lens,
-                  (codes, "codes", torch.uint8), scales, block_table, pos, stream)
+    _append_paged(_lib.mla_append_paged_q8, "mla_append_paged_q8", dims, c, k_r, new_offsets, seq_lens, codes, "codes",
+                  _U8, scales, block_table, pos, stream)
 
 
 def mla_decode_q8_workspace_size(dims, B: int, q_len: int = 1) -> int:
@@ -382,22 +375,31 @@ def mla_decode_absorbed_paged_q8(dims, weights: MLAWeights, codes, scales, block
     """Absorbed decode over the 8-bit paged cache: q_nope [B, q_len, H, 128], q_rope
     [B, q_len, H, 64], out [B, q_len, H, 128] (bf16); the q_len new tokens are the last q_len
     of each sequence's seq_lens[b] tokens, already appended."""
-    dev, bf, i32 = codes.device, torch.bfloat16, torch.int32
+    dev = codes.get_device()
+    if dev < 0:
+        raise ValueError(f"codes: on {codes.device}, not a CUDA device")
     if q_nope.dim() != 4:
         raise ValueError(f"q_nope: shape {tuple(q_nope.shape)}, not [B, q_len, H, qk_nope]")
-    B, Q, H, num_pages = q_nope.shape[0], q_nope.shape[1], dims.H, codes.shape[0]
-    qn = _tensor(q_nope, "q_nope", bf, (B, Q, H, dims.qk_nope), dev)
-    qr = _tensor(q_rope, "q_rope", bf, (B, Q, H, dims.d_hR), dev)
-    op = _tensor(out, "out", bf, (B, Q, H, dims.v_head), dev)
-    cd = _tensor(codes, "codes", torch.uint8, (num_pages, 64, dims.d_c + dims.d_hR), dev)
-    sc = _tensor(scales, "scales", torch.float32, (num_pages,), dev)
-    bt = _tensor(block_table, "block_table", i32, (B, block_table.shape[-1]), dev)
-    sl = _tensor(seq_lens, "seq_lens", i32, (B,), dev)
-    wp = _tensor(ws, "ws", torch.uint8, (ws.numel(),), dev)
-    with _on_device(dev, stream) as raw:
-        _check(_lib.mla_decode_absorbed_paged_q8(ctypes.byref(dims), weights.handle, qn, qr, cd, sc, num_pages, bt,
-                                                 block_table.shape[1], sl, B, Q, op, wp, ws.numel(), raw),
-               "mla_decode_absorbed_paged_q8")
+    B, Q, H, _ = q_nope.shape
+    num_pages, max_blocks, ws_bytes, d_hR = len(codes), block_table.shape[-1], ws.numel(), dims.d_hR
+    qn = _tensor(q_nope, "q_nope", _BF16, (B, Q, dims.H, dims.qk_nope), dev)
+    qr = _tensor(q_rope, "q_rope", _BF16, (B, Q, H, d_hR), dev)
+    op = _tensor(out, "out", _BF16, (B, Q, H, dims.v_head), dev)
+    cd = _tensor(codes, "codes", _U8, (num_pages, 64, dims.d_c + d_hR), dev)
+    sc = _tensor(scales, "scales", _F32, (num_pages,), dev)
+    bt = _tensor(block_table, "block_table", _I32, (B, max_blocks), dev)
+    sl = _tensor(seq_lens, "seq_lens", _I32, (B,), dev)
+    wp = _tensor(ws, "ws", _U8, (ws_bytes,), dev)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    before = _swap_device(dev)
+    try:
+        status = _lib.mla_decode_absorbed_paged_q8(ctypes.byref(dims), weights.handle, qn, qr, cd, sc, num_pages, bt,
+                                                   max_blocks, sl, B, Q, op, wp, ws_bytes, raw)
+    finally:
+        if before != dev:
+            _swap_device(before)
+    if status:
+        _check(status, "mla_decode_absorbed_paged_q8")
 
 
 def mla_prefill_causal(dims, weights: MLAWeights, h, W_DKV, W_KR, cache, out, ws, stream=None) -> None:
