@@ -1137,11 +1137,13 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // o_lat = sum_p 2^(m_p - m) l_p s_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
 // piece's normalised output in units of s_p.  One CTA per (head, 32 queries): W_UV[h] comes by
 // TMA before the wait for the attention kernel; sixteen warps merge two rows each into the B
-// operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), and D [128 x 32] =
-// W_UV[h] . o_lat^T takes both.
+// operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), rows r and 32 + r,
+// and the two halves of D [128 x 64] = W_UV[h] . o_lat^T are added as they are read.  (Two
+// products of 32 columns into one accumulator read W_UV from shared memory twice, which is what
+// bounds them.)
 constexpr int kMergeThreads = 512, kMergeN = 32;
-constexpr int kMergeA = 8 * 128 * 128, kMergeB = 8 * kMergeN * 128;
-constexpr int kMergeSmem = kMergeA + 2 * kMergeB + 64 + 1024;
+constexpr int kMergeA = 8 * 128 * 128, kMergeRows = 2 * kMergeN * 128, kMergeB = 8 * kMergeRows;
+constexpr int kMergeSmem = kMergeA + kMergeB + 64 + 1024;
 
 __global__ void __launch_bounds__(kMergeThreads, 1)
 merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws ws, __nv_bfloat16* __restrict__ out,
@@ -1149,7 +1151,7 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     extern __shared__ uint8_t merge_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)merge_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + kMergeA;
-    uint64_t* a_full = (uint64_t*)(sB + 2 * kMergeB);
+    uint64_t* a_full = (uint64_t*)(sB + kMergeB);
     uint64_t* d_full = a_full + 1;
     uint32_t* tmem_slot = (uint32_t*)(d_full + 1);
     const Shape& s = src.s;
@@ -1165,7 +1167,7 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         pdl_trigger();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(tmem_slot, kMergeN);
+        ptx::tmem_alloc(tmem_slot, 2 * kMergeN);
         ptx::tmem_relinquish();
     }
     // More than 8 queries: rows warp and warp + 16, both rows' requests in flight together.
@@ -1191,18 +1193,28 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 ml[2];        // statistics of the first 32 pieces (lane p)
     uint4 x[2][4][2];    // this warp's first four pieces
+    auto fetch = [&](int k, int q, size_t row) {
+        const uint4* from = (const uint4*)(ws.part_o + row * kDc + 16 * lane);
+        x[k][q][0] = from[0];
+        x[k][q][1] = from[1];
+    };
     auto request = [&](int k, int i0) {   // pieces share + shares (i0 .. i0 + 3)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int p = min(share + shares * (i0 + q), max(pc[k].y - 1, 0));
-            const uint4* from = (const uint4*)(ws.part_o + at(k, p) * kDc + 16 * lane);
-            x[k][q][0] = from[0];
-            x[k][q][1] = from[1];
+            const int p = share + shares * (i0 + q);
+            if (p > 0 && p < pc[k].y) fetch(k, q, at(k, p));
         }
     };
+    // the first piece's place is known without `pieces` (and holds nothing if there is none)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        ml[k] = lane < pc[k].y ? ws.part_ml[at(k, lane)] : none;
+        ml[k] = ws.part_ml[at(k, 0)];
+        if (share == 0) fetch(k, 0, at(k, 0));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (lane >= pc[k].y) ml[k] = none;
+        else if (lane > 0) ml[k] = ws.part_ml[at(k, lane)];
         request(k, 0);
     }
 #pragma unroll
@@ -1258,19 +1270,28 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine[32 * i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
             __syncthreads();
-            if (share == 0) {
-#pragma unroll 1
-                for (int o = 1; o < shares; ++o) {
-                    const float4* his = (const float4*)(sB + (warp + o) * 2048) + lane;
+            // words share * 512 / shares .. of the row are this warp's
+            const int n = 16 / shares, w0 = share * (512 / shares) + lane;
+            const float* all = (const float*)(sB + (warp - share) * 2048) + w0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = his[32 * i];
-                        acc[4 * i] += f.x, acc[4 * i + 1] += f.y, acc[4 * i + 2] += f.z, acc[4 * i + 3] += f.w;
-                    }
+            for (int i = 0; i < 8; ++i) {
+                acc[i] = 0.f;
+                if (i < n) {
+#pragma unroll 4
+                    for (int o = 0; o < shares; ++o) acc[i] += all[512 * o + 32 * i];
                 }
             }
             __syncthreads();   // the shares are read
-            if (share != 0) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) {   // word 128 u + 4 l + e is column 16 l + 4 u + e
+                    const int w = w0 + 32 * i, c = 16 * ((w >> 2) & 31) + 4 * (w >> 7) + (w & 3);
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(acc[i]), lo = __float2bfloat16_rn(acc[i] - __bfloat162float(hi));
+                    __nv_bfloat16* to = (__nv_bfloat16*)(sB + (c >> 6) * kMergeRows + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4)) + (c & 7);
+                    to[0] = hi;
+                    to[kMergeN * 64] = lo;
+                }
+            break;
         }
         // columns 16 lane .. +15 of row r: chunk lane / 4, 16-byte units 2 (lane % 4) and + 1
         uint32_t hi[8], lo[8];
@@ -1280,12 +1301,12 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
             lo[i] = ptx::pack_bf16(acc[2 * i] - __uint_as_float(hi[i] << 16),
                                    acc[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
         }
-        uint8_t* to = sB + (lane >> 2) * (kMergeN * 128) + r * 128;
+        uint8_t* to = sB + (lane >> 2) * kMergeRows + r * 128;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int u = ((2 * (lane & 3) + q) ^ (r & 7)) << 4;
             *(uint4*)(to + u) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-            *(uint4*)(to + kMergeB + u) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+            *(uint4*)(to + kMergeN * 128 + u) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
         }
     }
     ptx::fence_proxy_async_smem();   // read by the tensor cores
@@ -1298,16 +1319,13 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         if (!landed) latch(err, kErrTimeout, 9400000 + h);
         ptx::tc_fence_after();
         if (landed && elect()) {
-            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, kMergeN, 0, 0);
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, 2 * kMergeN, 0, 0);
 #pragma unroll 1
-            for (int term = 1; term >= 0; --term)
-#pragma unroll 1
-                for (int kc = 0; kc < 8; ++kc)
+            for (int kc = 0; kc < 8; ++kc)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem, ptx::desc_kmajor_sw128(ptx::smem_u32(sA + kc * 16384) + 32 * k),
-                                    ptx::desc_kmajor_sw128(ptx::smem_u32(sB + term * kMergeB + kc * kMergeN * 128) + 32 * k),
-                                    idesc, term == 0 || (kc | k) != 0);
+                for (int k = 0; k < 4; ++k)
+                    ptx::mma_ss(tmem, ptx::desc_kmajor_sw128(ptx::smem_u32(sA + kc * 16384) + 32 * k),
+                                ptx::desc_kmajor_sw128(ptx::smem_u32(sB + kc * kMergeRows) + 32 * k), idesc, (kc | k) != 0);
         }
         if (elect()) ptx::mma_commit(d_full);
     }
@@ -1319,11 +1337,13 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         // D (lane = output column, column = query) -> rows of 128 in the A buffer, then whole
         // 256-byte rows out[v, h, :]
         __nv_bfloat16* stage = (__nv_bfloat16*)sA;
-        uint32_t r[32];
+        uint32_t r[32], r2[32];
         ptx::tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), r);
+        ptx::tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + kMergeN, r2);
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) stage[j * 128 + warp * 32 + lane] = __float2bfloat16_rn(__uint_as_float(r[j]));
+        for (int j = 0; j < 32; ++j)
+            stage[j * 128 + warp * 32 + lane] = __float2bfloat16_rn(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
         ptx::named_barrier_sync(1, 128);
         for (int i = threadIdx.x; i < kMergeN * 16; i += 128) {
             const int v = n0 + (i >> 4);
@@ -1332,7 +1352,7 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 1) ptx::tmem_dealloc(tmem, kMergeN);
+    if (warp == 1) ptx::tmem_dealloc(tmem, 2 * kMergeN);
 }
 
 // Dynamic shared memory and the largest carve-out, once per kernel and device
