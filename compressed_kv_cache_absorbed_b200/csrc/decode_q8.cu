@@ -1135,7 +1135,8 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // ------------------------------------------------------------- merge and W_UV
 // out[v, h, :] = W_UV[h] o_lat[v, h, :],
 // o_lat = sum_p 2^(m_p - m) l_p s_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
-// piece's normalised output in units of s_p.  One CTA per (head, 32 queries): W_UV[h] comes by
+// piece's normalised output in units of s_p.  One CTA per (head, `per` queries), per = 32, or 16
+// or 8 where that still is one wave of CTAs (48 sequences, 16 heads: 43.2 -> 41.1 us): W_UV[h] comes by
 // TMA before the wait for the attention kernel; sixteen warps merge two rows each into the B
 // operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), rows r and 32 + r,
 // and the two halves of D [128 x 64] = W_UV[h] . o_lat^T are added as they are read.  (Two
@@ -1147,7 +1148,7 @@ constexpr int kMergeSmem = kMergeA + kMergeB + 64 + 1024;
 
 __global__ void __launch_bounds__(kMergeThreads, 1)
 merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws ws, __nv_bfloat16* __restrict__ out,
-             const DevErr err) {
+             int per, const DevErr err) {
     extern __shared__ uint8_t merge_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)merge_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + kMergeA;
@@ -1155,7 +1156,7 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     uint64_t* d_full = a_full + 1;
     uint32_t* tmem_slot = (uint32_t*)(d_full + 1);
     const Shape& s = src.s;
-    const int h = blockIdx.x, n0 = blockIdx.y * kMergeN, NV = s.B * s.q_len;
+    const int h = blockIdx.x, n0 = blockIdx.y * per, NV = s.B * s.q_len;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         ptx::mbar_init(a_full, 1);
@@ -1170,11 +1171,11 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         ptx::tmem_alloc(tmem_slot, 2 * kMergeN);
         ptx::tmem_relinquish();
     }
-    // More than 8 queries: rows warp and warp + 16, both rows' requests in flight together.
-    // Fewer: `shares` warps take every shares-th piece of one row each (a row of one long
+    // More than 16 queries: rows warp and warp + 16, both rows' requests in flight together.
+    // 8 or fewer: `shares` warps take every shares-th piece of one row each (a row of one long
     // sequence has a piece per CTA).
-    const int rows = min(kMergeN, NV - n0);
-    const int shares = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16, share = warp % shares;
+    const int rows = min(per, NV - n0);
+    const int shares = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16, share = warp % shares, mine = rows > 16 ? 2 : 1;
     int item[2], rin[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -1186,7 +1187,8 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     pdl_wait();   // the partials come from the attention kernel
     int2 pc[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) pc[k] = ws.pieces[item[k]];
+    for (int k = 0; k < 2; ++k)
+        if (k < mine) pc[k] = ws.pieces[item[k]];
     auto at = [&](int k, int p) -> size_t {   // row of part_o and part_ml
         return (size_t)(p == 0 ? item[k] : pc[k].x + (p - 1) * s.sib) * s.R + rin[k];
     };
@@ -1208,18 +1210,20 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
     // the first piece's place is known without `pieces` (and holds nothing if there is none)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+        if (k >= mine) break;
         ml[k] = ws.part_ml[at(k, 0)];
         if (share == 0) fetch(k, 0, at(k, 0));
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+        if (k >= mine) break;
         if (lane >= pc[k].y) ml[k] = none;
         else if (lane > 0) ml[k] = ws.part_ml[at(k, lane)];
         request(k, 0);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        if (shares > 1 && k > 0) break;
+        if (k >= mine) break;
         const int r = shares > 1 ? warp / shares : warp + 16 * k, np = pc[k].y;
         float acc[16];
 #pragma unroll
@@ -1266,9 +1270,9 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] *= inv;
         if (shares > 1) {   // the shares of a row meet in shared memory, and are added in order
-            float4* mine = (float4*)(sB + warp * 2048) + lane;
+            float4* to4 = (float4*)(sB + warp * 2048) + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mine[32 * i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) to4[32 * i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
             __syncthreads();
             // words share * 512 / shares .. of the row are this warp's
             const int n = 16 / shares, w0 = share * (512 / shares) + lane;
@@ -1347,7 +1351,7 @@ merge_kernel(const __grid_constant__ CUtensorMap tm_w, const Src src, const Ws w
         ptx::named_barrier_sync(1, 128);
         for (int i = threadIdx.x; i < kMergeN * 16; i += 128) {
             const int v = n0 + (i >> 4);
-            if (v < NV) ((uint4*)(out + ((size_t)v * s.H + h) * 128))[i & 15] = ((const uint4*)sA)[i];
+            if ((i >> 4) < rows) ((uint4*)(out + ((size_t)v * s.H + h) * 128))[i & 15] = ((const uint4*)sA)[i];
         }
     }
     ptx::tc_fence_before();
@@ -1449,8 +1453,10 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
     if (!make_tmap_bf16(&mv, p.W_UV, 2, dv, sv, bv)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     if ((e = set_smem(merge_kernel, kMergeSmem, done)) != cudaSuccess) return e;
-    return launch_pdl(merge_kernel, dim3(s.H, (unsigned)((NV + kMergeN - 1) / kMergeN)), dim3(kMergeThreads), kMergeSmem,
-                      st, mv, src, ws, p.out, err);
+    int per = kMergeN;
+    while (per > 8 && (long long)s.H * ((NV + per / 2 - 1) / (per / 2)) <= s.ctas) per /= 2;
+    return launch_pdl(merge_kernel, dim3(s.H, (unsigned)((NV + per - 1) / per)), dim3(kMergeThreads), kMergeSmem, st, mv,
+                      src, ws, p.out, per, err);
 }
 
 cudaError_t set_wait_limit_decode_q8(uint32_t polls) { return ptx::set_wait_limit_of_this_file(polls); }
