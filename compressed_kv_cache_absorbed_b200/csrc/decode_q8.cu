@@ -1136,12 +1136,11 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // out[v, h, :] = W_UV[h] o_lat[v, h, :],
 // o_lat = sum_p 2^(m_p - m) l_p s_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
 // piece's normalised output in units of s_p.  One CTA per (head, `per` queries), per = 32, or 16
-// or 8 where that still is one wave of CTAs (48 sequences, 16 heads: 43.2 -> 41.1 us): W_UV[h] comes by
-// TMA before the wait for the attention kernel; sixteen warps merge two rows each into the B
+// or 8 where that still is one wave of CTAs (48 sequences, 16 heads: 43.2 -> 41.1 us).  W_UV[h]
+// comes by TMA before the wait for the attention kernel; sixteen warps merge the rows into the B
 // operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), rows r and 32 + r,
-// and the two halves of D [128 x 64] = W_UV[h] . o_lat^T are added as they are read.  (Two
-// products of 32 columns into one accumulator read W_UV from shared memory twice, which is what
-// bounds them.)
+// and the two halves of D [128 x 64] = W_UV[h] . o_lat^T are added as they are read: W_UV leaves
+// shared memory once.  Latency bounds it: the list of pieces, their statistics and outputs.
 constexpr int kMergeThreads = 512, kMergeN = 32;
 constexpr int kMergeA = 8 * 128 * 128, kMergeRows = 2 * kMergeN * 128, kMergeB = 8 * kMergeRows;
 constexpr int kMergeSmem = kMergeA + kMergeB + 64 + 1024;

@@ -370,7 +370,8 @@ size_t mla_decode_q8_workspace_size(const mla_dims* dims, int32_t B, int32_t q_l
  *   q_nope [B, q_len, H, 128], q_rope [B, q_len, H, 64] (rotated), out [B, q_len, H, 128]:
  *   device, bf16, contiguous, 16-byte aligned; codes 16-byte aligned.
  * Any head count up to 128 (a head-parallel layer's share of the heads), bf16, d_c = 512,
- * d_hR = 64, qk_nope = v_head = 128 and handles without W_O, else MLA_ERR_UNSUPPORTED.  The
+ * d_hR = 64, qk_nope = v_head = 128, handles without W_O, B * q_len <= 65535 and caches of
+ * fewer than 2^31 rows, else MLA_ERR_UNSUPPORTED.  The
  * scales of the pages in use must be positive and finite (any such value, not only powers of
  * two).  What the pages hold behind a sequence's last token does not matter, NaN codes
  * included.  A token with no key gets zeros.  A sequence with a negative length or more than

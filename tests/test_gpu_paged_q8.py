@@ -288,6 +288,15 @@ def test_decode_lengths(H, Q, lens):
     Decode(H, Q, lens, seed=77).check(f"H={H} q_len={Q} B={len(lens)}")
 
 
+@pytest.mark.parametrize("B", [1, 2, 3, 5, 8, 9, 16, 17, 33])
+@pytest.mark.parametrize("H", [16, 70, 128])
+def test_decode_numbers_of_queries(H, B):
+    """Rows of a merge CTA: one, a few (shared by warps), up to 16, up to 32, a rest; each with
+    sequences of one piece and of many, and one without tokens."""
+    lens = [3000 if i % 3 == 0 else 0 if i % 7 == 4 else 90 + i for i in range(B)]
+    Decode(H, 1, lens, seed=B).check(f"H={H} B={B}")
+
+
 @pytest.mark.parametrize("exps", [(0, 3, -4), (-40,), (40,), (0.37, -1.9), (0, 12)])
 @pytest.mark.parametrize("H", [16, 128])
 def test_decode_scales_of_the_pages(H, exps):
