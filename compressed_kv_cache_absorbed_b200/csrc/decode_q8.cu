@@ -54,7 +54,8 @@ constexpr int kRopeBytes = kT * kDr;          // the rotary columns of a tile (6
 constexpr int kRoleThreads = 128;             // TMA warp, score issuer, O issuer, the warp that finds the pieces
 // Cost units of a piece's query load and epilogue, in tiles: 1.  With 2, which is nearer to what
 // a switch takes, the longest ranges are as long and the step no faster (128 heads, 32 x 4096:
-// 66.2 and 66.5 us; 100-token chunks: 141.2 and 143.8; ragged long contexts: 321 and 320).
+// 66.2 and 66.5 us; 100-token chunks: 141.2 and 143.8; ragged long contexts: 321 and 320).  Nor
+// did a split in quarter tiles that charges two: 64.1 and 63.9 us, 16 heads 43.7 and 44.9.
 constexpr int kPieceCost = 1;
 // Up to this many groups of a sequence are walked side by side, so that its pages come from HBM
 // once and from L2 for the others.  Side by side and one after another: 2 groups 66.2 and 67.6
@@ -67,9 +68,9 @@ constexpr float kFarLog2 = 64.f;              // how far below its highest value
 
 // Shared memory: NC chunk slots (as many as fit), NR slots that hold a tile's rotary columns and
 // then its P (hi and, for R <= 32, lo), P's lo term (R = 64), the group's queries.  (Slots of their
-// own for the rotary columns, free once the scores are made, changed nothing; nor did bringing
-// the pages into L2 two tiles ahead: 321 -> 320 us on ragged long contexts, 51 -> 54 us with 16
-// heads.)
+// own for the rotary columns, free once the scores are made, changed nothing.  Pages brought into
+// L2 two tiles ahead make a tile's cycles fewer, 3704 -> 3184, but not the time: 315.7 -> 313.3 us
+// on ragged long contexts, 137.2 -> 138.3 on chunks; the clock falls with the power.)
 // Softmax warps: four (one per 32 tokens) for each of CG groups of HC rows; 16 rows a thread
 // keep its scores, sums and references in registers beside four warps per scheduler.
 template <int R> struct Cfg {
