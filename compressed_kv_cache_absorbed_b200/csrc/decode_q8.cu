@@ -6,33 +6,37 @@
 // over the first seq_lens[b] - q_len + t + 1 tokens, then out[r] = W_UV[h] o_lat[r].
 //
 // The codes are MMA operands as they are (kind::f8f6f4, E4M3); nothing is dequantised.  The
-// other operand of each product keeps 16-bit precision as the sum of two E4M3 terms: with
-// hi = e4m3(x) and lo = e4m3(x - hi), hi + lo is within 2^-8 |x| of x (half a step of 4 bits
-// twice), which is a bf16 rounding.  Two 8-bit products cost what one 16-bit product does.
+// other operand of each product is a sum of 8-bit terms.  A query value is two E4M3 terms against
+// its row's largest value: hi = e4m3(x) and lo = e4m3(x - hi) leave 2^-8 |x| (half a step of 4
+// bits twice), or 2^-17 of the row's largest value where that is more.  A probability must keep its
+// precision however small it is beside its tile's largest: a token that takes most of the weight
+// may carry no value (an attention sink), and then the small ones make up the output.  It is three
+// E5M2 terms, each of what the ones before it left, times 8 from term to term: p = t0 + t1 / 8 + t2 / 64
+// within 2^-9 p (half a step of 3 bits three times) + 2^-11 p (fp16, in which they are made) for
+// p >= 2^-14, and 2^-23 below.  The terms are columns of one product, each with its own accumulator.
 //
-// Tokens are the MMA's M.  A tile is 128 tokens (two pages); a group is R <= 64 query rows:
+// Tokens are the MMA's M.  A tile is 128 tokens (two pages); a group is R <= 32 query rows:
 //     S^T [128 tokens x 2R]  = codes [128 x 576] . [q_hi | q_lo]^T      (both terms in one product)
-//     O^T [4 x 128 latents x R] += codes^T [512 x 128] . P [128 x R]    (hi and lo)
+//     O^T [4 x 128 latents x 3R] += codes^T [512 x 128] . P [128 x 3R]  (all three terms in one)
 // so the codes are the A operand of both, K-major for the scores and MN-major for O, from the
-// one copy in shared memory; 64 rows' O takes 256 TMEM columns, two score buffers the other
-// 256, and a CTA needs no other CTA's scores.  A thread of the softmax holds one token and 16
-// rows (8 for R = 16): P goes to shared memory in the layout the product reads, sums stay per
+// one copy in shared memory; 32 rows' O takes 384 TMEM columns, two score buffers the other
+// 128, and a CTA needs no other CTA's scores.  A thread of the softmax holds one token and 8
+// rows: P goes to shared memory in the layout the product reads, sums stay per
 // thread until the end of a piece, and the only thing the token lanes must agree on is each
 // row's reference M (below).
 //
-// What bounds it.  R = 64: a tile is 18 score products of N = 128 (65 cycles each) and 32 O
-// products of N = 64 (48.5: the A operand's 4 KB from shared memory, not the arithmetic), 2770
-// cycles together; it takes ~3700, because scores of tile g + 2 need the slots that O of tile g
-// frees and their own loads (two tiles fit beside the queries), then 2300 cycles of softmax: a
-// loop of 7400 cycles over two tiles.  Measured, 128 heads, 32 sequences of 4096 tokens: 48.2 us
-// (82.4 k cycles, tensor pipe 49 % of them, 80 MB from DRAM); 16 heads, 48 ragged sequences of
-// 4500 tokens on average: 29.5 us, 119 MB, 62 % of a copy's bandwidth, the rest start and end.
+// What bounds it.  A tile's 18 score products (N = 64) and 16 O products (N = 96) are each bound by
+// the A operand's 4 KB from shared memory.  Two tiles are in flight (two score buffers, two P
+// slots), and a tile's loads, scores, softmax and O follow one another.
 //
-// The reference.  p = 2^(z' - M) must fit E4M3 (<= 448) and must not sink into its subnormals
-// (step 2^-9), so M follows the scores in both directions: it is set so that the tile's
-// largest p is 2^5, and set anew (O and the sums rescaled) when a tile's largest p leaves
-// [1, 2^8.5].  A one-sided running maximum, enough for a wider type, would leave everything
-// behind one dominating token to the subnormals.  The pages' scales ride on the
+// The reference.  p = 2^-6 2^(z' - M) must fit fp16 and E5M2 and must not sink below them, so M
+// follows the scores in both directions: it is set so that the tile's largest p is 2^4, and set
+// anew (O and the sums rescaled) when a tile's largest p leaves [2^-6, 2^15.5].  The row's largest
+// so far is thus at 2^4 or above: what is 2^-18 of it keeps all of P's bits, and the least step
+// is 2^-27 of it.  A new reference costs a wait for the O product before and a pass over O, so the
+// window is as wide as those bits allow and its set point leaves most of the room above, where new
+// maxima come: with scores of 3 nats' spread, 32 sequences of 4096 tokens, 128 heads, 74.9 us, and 84.0
+// with the window [2^4, 2^15.5] set at 2^10.  The pages' scales ride on the
 // probabilities: z' = z + log2(s_j / s_ref) with s_ref the piece's first page's scale.
 #include <math.h>
 
@@ -52,40 +56,36 @@ constexpr int kT = 128;                       // tokens per tile
 constexpr int kChunkBytes = kT * 128;         // 128 latent columns of a tile (128-byte swizzle)
 constexpr int kRopeBytes = kT * kDr;          // the rotary columns of a tile (64-byte swizzle)
 constexpr int kRoleThreads = 128;             // TMA warp, score issuer, O issuer, the warp that finds the pieces
-// Cost units of a piece's query load and epilogue, in tiles: 1.  With 2, which is nearer to what
-// a switch takes, the longest ranges are as long and the step no faster (128 heads, 32 x 4096:
-// 66.2 and 66.5 us; 100-token chunks: 141.2 and 143.8; ragged long contexts: 321 and 320).  Nor
-// did a split in quarter tiles that charges two: 64.1 and 63.9 us, 16 heads 43.7 and 44.9.
+// Cost units of a piece's query load and epilogue, in tiles: 1.  With 2 the longest ranges are as
+// long and the step no faster (graph replays; 128 heads, 32 x 4096 tokens: 69.7 and 69.9 us; 100-token
+// chunks: 147.3 and 147.2; ragged long contexts: 420.7 and 419.4).
 constexpr int kPieceCost = 1;
 // Up to this many groups of a sequence are walked side by side, so that its pages come from HBM
-// once and from L2 for the others.  Side by side and one after another: 2 groups 66.2 and 67.6
-// us, 64 ragged sequences of up to 32768 tokens 321 and 349; 8 groups 106.4 and 106.9; 10 groups
-// 133.9 and 132.2, where 148 CTAs no longer divide well by the groups.
+// once and from L2 for the others.  Side by side and one after another: 4 groups 69.7 and 72.0
+// us, 64 ragged sequences of up to 32768 tokens 421 and 528; 8 groups 120.4 and 123.6.
 constexpr int kMaxSib = 8;
-constexpr float kTopLog2 = 8.5f;              // p <= 2^8.5
-constexpr float kSetLog2 = 5.f;               // a new reference puts the tile's largest p here
+constexpr float kPGain = 1.f / 64;            // p = 2^-6 2^(z' - M)
+constexpr float kTopLog2 = 21.5f;             // p <= 2^15.5 (the largest E5M2 value is 1.75 x 2^15)
+constexpr float kSetLog2 = 10.f;              // a new reference puts the tile's largest p at 2^4
 constexpr float kFarLog2 = 64.f;              // how far below its highest value a reference may go
 
 // Shared memory: NC chunk slots (as many as fit), NR slots that hold a tile's rotary columns and
-// then its P (hi and, for R <= 32, lo), P's lo term (R = 64), the group's queries.  (Slots of their
-// own for the rotary columns, free once the scores are made, changed nothing.  Pages brought into
-// L2 two tiles ahead make a tile's cycles fewer, 3704 -> 3184, but not the time: 315.7 -> 313.3 us
-// on ragged long contexts, 137.2 -> 138.3 on chunks; the clock falls with the power.)
-// Softmax warps: four (one per 32 tokens) for each of CG groups of HC rows; 16 rows a thread
-// keep its scores, sums and references in registers beside four warps per scheduler.
+// then its P (three terms of R bytes per token), the group's queries.
+// Softmax warps: four (one per 32 tokens) for each of CG groups of HC rows.
 template <int R> struct Cfg {
-    static constexpr int HC = R == 16 ? 8 : 16, CG = R / HC;
+    static constexpr int HC = 8, CG = R / HC;
     static constexpr int kSoft = 128 * CG, kThreads = kRoleThreads + kSoft;
-    static constexpr bool kTwoPass = R == 64;            // P hi and lo as two products (one accumulator)
-    static constexpr int NP = kTwoPass ? R : 2 * R;      // N of an O product
-    static constexpr int NC = R == 64 ? 8 : 10;
+    static constexpr int kTerms = 3, NP = kTerms * R;    // N of an O product
+    static constexpr int kPRow = R == 32 ? 128 : 64;     // bytes of a token's P, swizzled over as many
+    static constexpr int NC = R == 32 ? 9 : 10;
     static constexpr int NR = 2;
-    static constexpr int kLoBytes = kTwoPass ? kRopeBytes : 0;
+    static constexpr int kSlotBytes = kT * kPRow;
     static constexpr int kQBytes = 2 * R * kRow;
     static constexpr uint32_t kColO = 4 * R;
     static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
     static constexpr int kMisc = 3 * 1024;
-    static constexpr int kSmem = NC * kChunkBytes + NR * kRopeBytes + kLoBytes + kQBytes + kMisc;
+    static constexpr int kSmem = NC * kChunkBytes + NR * kSlotBytes + kQBytes + kMisc;
+    static_assert(NP <= kPRow && kRopeBytes <= kSlotBytes, "a tile's P or rotary columns in a slot");
     static_assert(kColO + 4 * NP <= kTmemCols, "TMEM columns");
     static_assert(kSmem <= 232448, "shared memory over the 227 KB limit");
 };
@@ -120,9 +120,9 @@ __device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu,
 // version 1, swizzle (2: 128 bytes, 4: 64 bytes)
 __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle << 29); }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
-// E4M3 x E4M3 -> fp32
-constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major, int b_mn_major) {
-    return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+// E4M3 x E4M3 (b_format 0) or E5M2 (1) -> fp32
+constexpr uint32_t idesc_f8(int M, int N, int b_format, int a_mn_major, int b_mn_major) {
+    return (1u << 4) | ((uint32_t)b_format << 10) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
@@ -137,7 +137,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) { ptx::tmem_st16(taddr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -187,30 +186,28 @@ __device__ __forceinline__ uint32_t e4m3x2_f32(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// four fp16 values <-> four E4M3 codes
-__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b) {
+// four fp16 values -> four E5M2 codes (nearest even, saturating, NaN kept)
+__device__ __forceinline__ uint32_t e5m2x4(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e5m2x2.f16x2 x, %1;\n\tcvt.rn.satfinite.e5m2x2.f16x2 y, %2;\n\t"
         "mov.b32 %0, {x, y};\n\t}"
         : "=r"(r)
         : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ void f16x4(uint32_t codes, uint32_t& a, uint32_t& b) {
-    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-        : "=r"(a), "=r"(b)
-        : "r"(codes));
+// 8 (x - t), x two fp16 values and t their E5M2 codes, which are fp16's upper bytes (bytes `sel`
+// of `codes`); exact unless it is below fp16's normal numbers
+__device__ __forceinline__ uint32_t rest_of(uint32_t x, uint32_t codes, uint32_t sel) {
+    const uint32_t t = __byte_perm(codes, 0, sel);
+    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&t)),
+                              __float2half2_rn(8.f));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t code2) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)code2));
     return h;
 }
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // ---------------------------------------------------------------- work split
 // As in the other decode kernels: the tiles of all sequences, in order, are cut into equal
 // ranges; a range may hold pieces of several sequences.  A virtual sequence is a sequence
@@ -306,13 +303,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     }
     uint8_t* chunks = smem;
     uint8_t* ropes = chunks + NC * kChunkBytes;
-    uint8_t* plo = ropes + NR * kRopeBytes;
-    uint8_t* qimg = plo + C::kLoBytes;
+    uint8_t* qimg = ropes + NR * C::kSlotBytes;
     float* qs = (float*)(qimg + C::kQBytes);            // [R] row scales of the queries
-    float4* red = (float4*)(qs + 64);                   // [CG][16] per row, one value per token quarter
+    float4* red = (float4*)(qs + 32);                   // [CG][16] per row, one value per token quarter
     float* nrefs = (float*)(red + 64);                  // [R] each row's reference, negated
-    float* row_kt = nrefs + 64;                         // [R] row scale x softmax scale x the piece's first page's scale
-    uint64_t* bars = (uint64_t*)(row_kt + 64);
+    float* row_kt = nrefs + 32;                         // [R] row scale x softmax scale x the piece's first page's scale
+    uint64_t* bars = (uint64_t*)(row_kt + 32);
     uint64_t *chunk_full = bars, *chunk_empty = bars + NC, *rope_full = bars + 2 * NC, *rope_empty = rope_full + 2;
     uint64_t *q_full = rope_full + 4, *s_full = rope_full + 5, *s_free = rope_full + 7, *p_ready = rope_full + 9;
     uint64_t *o_done = rope_full + 12, *grp_bar = rope_full + 14, *drain = rope_full + 18;
@@ -323,8 +319,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     float* out_scale = page_scale + 8;                  // [CG][4] largest page scale a warp saw
     uint32_t* tmem_slot = (uint32_t*)(out_scale + 16);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-    static_assert(64 * 4 + 64 * 16 + 128 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
-    static_assert(NC % 2 == 0, "16-byte alignment of the words behind the barriers");
+    static_assert(32 * 4 + 64 * 16 + 64 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NC; ++i) {
@@ -432,7 +427,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 if (ok && elect()) {
                     page_scale[2 * (g & 3)] = s0;
                     page_scale[2 * (g & 3) + 1] = s1;
-                    uint8_t* dst = ropes + (g % NR) * kRopeBytes;
+                    uint8_t* dst = ropes + (g % NR) * C::kSlotBytes;
                     ptx::mbar_expect_tx(&rope_full[g % NR], kRopeBytes);
                     ptx::tma_load_2d_hint(dst, &tm_rope, &rope_full[g % NR], kDc, r0, policy);
                     ptx::tma_load_2d_hint(dst + kRopeBytes / 2, &tm_rope, &rope_full[g % NR], kDc, r1, policy);
@@ -452,7 +447,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ---------------------------------------------- queries and score products
-        constexpr uint32_t idesc = idesc_e4m3(128, 2 * R, 0, 0);
+        constexpr uint32_t idesc = idesc_f8(128, 2 * R, 0, 0, 0);
         constexpr uint32_t h128 = desc_hi(1024, 2), h64 = desc_hi(512, 4);
         const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), 16), rope0 = desc_lo(ptx::smem_u32(ropes), 16),
                        q0 = desc_lo(ptx::smem_u32(qimg), 16);
@@ -492,7 +487,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 }
                 if (!ok || !wait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }
                 ptx::tc_fence_after();
-                const uint32_t a = rope0 + (g % NR) * (kRopeBytes >> 4), b = q0 + 4 * (2 * R * 128 >> 4);
+                const uint32_t a = rope0 + (g % NR) * (C::kSlotBytes >> 4), b = q0 + 4 * (2 * R * 128 >> 4);
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) mma_f8(d, a + 2 * k, h64, b + 2 * k, h64, idesc, 1);
@@ -505,10 +500,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         if (!ptx::mbar_wait(drain, 0, nullptr)) fail(err, abort_flag, 14);
     } else if (warp == 2) {
         // ---------------------------------------------------------- O products
-        constexpr uint32_t idesc = idesc_e4m3(128, C::NP, 1, 1);
-        constexpr uint32_t h128 = desc_hi(1024, 2), h64 = desc_hi(512, 4);
-        const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), kChunkBytes), rope0 = desc_lo(ptx::smem_u32(ropes), 512),
-                       lo0 = desc_lo(ptx::smem_u32(plo), 512);
+        constexpr uint32_t idesc = idesc_f8(128, C::NP, 1, 1, 1);
+        constexpr uint32_t h128 = desc_hi(1024, 2), hp = C::kPRow == 128 ? h128 : desc_hi(512, 4);
+        const uint32_t chunk0 = desc_lo(ptx::smem_u32(chunks), kChunkBytes),
+                       p0 = desc_lo(ptx::smem_u32(ropes), C::kSlotBytes);
         uint32_t g = 0, slot0 = 0;
         bool ok = true;
         while (ok && next_piece()) {
@@ -517,7 +512,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             for (int left = uniform(sg.j1 - sg.j0); left > 0; --left, ++g) {
                 if (!wait_warp(&p_ready[g & 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
                 ptx::tc_fence_after();
-                const uint32_t p = rope0 + (g % NR) * (kRopeBytes >> 4);
+                const uint32_t p = p0 + (g % NR) * (C::kSlotBytes >> 4);
                 // chunk by chunk, so that the first slots are free for the next loads early
                 if (elect()) {
                     uint32_t slot = slot0;
@@ -526,12 +521,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                         const uint32_t a = chunk0 + slot * (kChunkBytes >> 4), d = tmem + C::kColO + c * C::NP;
 #pragma unroll
                         for (int k = 0; k < kT / 32; ++k)
-                            mma_f8(d, a + 256 * k, h128, p + 128 * k, h64, idesc, acc0 | (k > 0));
-                        if (C::kTwoPass) {
-#pragma unroll
-                            for (int k = 0; k < kT / 32; ++k)
-                                mma_f8(d, a + 256 * k, h128, lo0 + 128 * k, h64, idesc, 1);
-                        }
+                            mma_f8(d, a + 256 * k, h128, p + (32 * C::kPRow >> 4) * k, hp, idesc, acc0 | (k > 0));
                         ptx::mma_commit(&chunk_empty[slot]);
                         slot = slot + 1 == NC ? 0 : slot + 1;
                     }
@@ -570,10 +560,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 const bool first = j == sg.j0;
                 if (first && !uwait(q_full, piece & 1)) { ok = false; break; }   // row scales
                 if (!uwait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }   // page scales
-                // O of tile g - 2 is done, whose P lay where this tile's goes (R = 64 waits for tile
-                // g - 1 below).  Every phase of a barrier is waited for, so that a later wait cannot
-                // take an older one for its own.
-                if (!C::kTwoPass && g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
+                // O of tile g - 2 is done, whose P lay where this tile's goes.  Every phase of a
+                // barrier is waited for, so that a later wait cannot take an older one for its own.
+                if (g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
                 float s = page_scale[2 * (g & 3) + (quad >> 1)];
                 if (first) {
                     const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
@@ -645,7 +634,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     }
                 }
                 // Does every row keep its reference?  Sign bits of the arguments, anded over the
-                // tile's tokens, name the rows whose largest p is below 1; any argument past the
+                // tile's tokens, name the rows whose largest p is below 2^-6; any argument past the
                 // top sends the warp's word to "all".
                 {
                     uint32_t low = 0;
@@ -704,22 +693,28 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
 #pragma unroll
                         for (int i = 0; i < HC / 2; ++i)
                             l[i] = mul2(l[i], pair(__shfl_sync(0xffffffffu, alpha, 2 * i), __shfl_sync(0xffffffffu, alpha, 2 * i + 1)));
+                        float al[HC];
+#pragma unroll
+                        for (int i = 0; i < HC; ++i) al[i] = __shfl_sync(0xffffffffu, alpha, i);
 #pragma unroll 1
-                        for (int c = 0; c < 4 * (C::NP / R); ++c) {
-                            uint32_t r[HC];
-                            const uint32_t ad = lane_addr + C::kColO + c * R + c0;
-                            tmem_ld(ad, r);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[C::kTerms][HC];
+                            const uint32_t ad = lane_addr + C::kColO + c * C::NP + c0;
+#pragma unroll
+                            for (int t = 0; t < C::kTerms; ++t) tmem_ld(ad + t * R, r[t]);
                             ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < HC; ++i)
-                                r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, alpha, i));
-                            tmem_st(ad, r);
+                            for (int t = 0; t < C::kTerms; ++t) {
+#pragma unroll
+                                for (int i = 0; i < HC; ++i) r[t][i] = __float_as_uint(__uint_as_float(r[t][i]) * al[i]);
+                                tmem_st(ad + t * R, r[t]);
+                            }
                         }
                         ptx::tmem_wait_st();
                     }
                 }
-                // P in two E4M3 terms; the sums take the unrounded p
-                uint32_t hi8[HC / 4], lo8[HC / 4];
+                // P in three E5M2 terms; the sums take 2^(z - M), not rounded
+                uint32_t p8[C::kTerms][HC / 4];
                 const f32x2 back2 = pair(back, back);
 #pragma unroll
                 for (int i = 0; i < HC / 4; ++i) {
@@ -730,27 +725,24 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     for (int q = 0; q < 4; ++q) x[q] = ex2(x[q]);
                     l[2 * i] = fma2(pair(x[0], x[1]), back2, l[2 * i]);
                     l[2 * i + 1] = fma2(pair(x[2], x[3]), back2, l[2 * i + 1]);
-                    const uint32_t v0 = ptx::pack_f16(x[0], x[1]), v1 = ptx::pack_f16(x[2], x[3]);
-                    uint32_t f0, f1;
-                    hi8[i] = e4m3x4(v0, v1);
-                    f16x4(hi8[i], f0, f1);
-                    lo8[i] = e4m3x4(hsub2(v0, f0), hsub2(v1, f1));
+                    uint32_t v0 = ptx::pack_f16(x[0] * kPGain, x[1] * kPGain), v1 = ptx::pack_f16(x[2] * kPGain, x[3] * kPGain);
+#pragma unroll
+                    for (int t = 0; t < C::kTerms; ++t) {
+                        p8[t][i] = e5m2x4(v0, v1);
+                        if (t + 1 < C::kTerms) {
+                            v0 = rest_of(v0, p8[t][i], 0x1404);
+                            v1 = rest_of(v1, p8[t][i], 0x3424);
+                        }
+                    }
                 }
-                // row tok of P: 64 bytes, 16-byte unit u at u ^ (tok / 2 % 4)
-                uint8_t* prow = ropes + (g % NR) * kRopeBytes + tok * 64;
-                const int sw = (tok >> 1) & 3;
-                if (C::kTwoPass) {
-                    // one buffer for the lo terms: O of the tile before is done with it
-                    if (g > 0 && !uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
-                    const int at = tok * 64 + ((grp ^ sw) << 4);
-                    *(uint4*)(ropes + (g % NR) * kRopeBytes + at) = make_uint4(hi8[0], hi8[1], hi8[HC / 8], hi8[HC / 4 - 1]);
-                    *(uint4*)(plo + at) = make_uint4(lo8[0], lo8[1], lo8[HC / 8], lo8[HC / 4 - 1]);
-                } else if (R == 32) {
-                    *(uint4*)(prow + ((grp ^ sw) << 4)) = make_uint4(hi8[0], hi8[1], hi8[HC / 8], hi8[HC / 4 - 1]);
-                    *(uint4*)(prow + (((2 + grp) ^ sw) << 4)) = make_uint4(lo8[0], lo8[1], lo8[HC / 8], lo8[HC / 4 - 1]);
-                } else {
-                    *(uint2*)(prow + ((0 ^ sw) << 4) + 8 * grp) = make_uint2(hi8[0], hi8[1]);
-                    *(uint2*)(prow + ((1 ^ sw) << 4) + 8 * grp) = make_uint2(lo8[0], lo8[1]);
+                // row tok of P: columns t R + c0 .. + 7, 16-byte unit u at u ^ (tok mod 8) in 128-byte
+                // rows, u ^ (tok / 2 mod 4) in 64-byte ones
+                uint8_t* prow = ropes + (g % NR) * C::kSlotBytes + tok * C::kPRow;
+                const int sw = C::kPRow == 128 ? tok & 7 : (tok >> 1) & 3;
+#pragma unroll
+                for (int t = 0; t < C::kTerms; ++t) {
+                    const int at = t * R + c0;
+                    *(uint2*)(prow + (((at >> 4) ^ sw) << 4) + (at & 8)) = make_uint2(p8[t][0], p8[t][1]);
                 }
                 if (edge) {
                     // Rows that some row of the group must not see may hold NaN codes (what lies
@@ -794,7 +786,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 }
             }
             // row held by this lane: the lane bits from 16 down, as many as HC has
-            const int my_row = lane >> (HC == 16 ? 1 : 2);
+            const int my_row = lane >> 2;
             float* sums = (float*)(red + grp * 16);   // [4 quarters][16]
             meet();   // red is read
             if (!ok) break;
@@ -810,7 +802,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             float f = 0.f;   // lane i: what turns row c0 + i of O into its normalised output
             if (lane < HC) {
                 const float t = (sums[lane] + sums[16 + lane]) + (sums[32 + lane] + sums[48 + lane]);
-                f = t != 0.f ? (s_ref / s_out) / t : 0.f;
+                f = t != 0.f ? (s_ref / s_out) / (kPGain * t) : 0.f;
                 if (quad == 0) ws.part_ml[(size_t)sg.slot * R + c0 + lane] = make_float4(m_row, t, s_out, 0.f);
             }
             // (a warp's store is 64 contiguous bytes; turning the tile around with shuffles for
@@ -821,19 +813,15 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             for (int i = 0; i < HC; ++i) fr[i] = __shfl_sync(0xffffffffu, f, i);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t r[HC];
-                tmem_ld(lane_addr + C::kColO + c * C::NP + c0, r);
-                if (C::NP > R) {
-                    uint32_t r2[HC];
-                    tmem_ld(lane_addr + C::kColO + c * C::NP + R + c0, r2);
-                    ptx::tmem_wait_ld();
+                uint32_t r[C::kTerms][HC];
 #pragma unroll
-                    for (int i = 0; i < HC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
-                } else {
-                    ptx::tmem_wait_ld();
+                for (int t = 0; t < C::kTerms; ++t) tmem_ld(lane_addr + C::kColO + c * C::NP + t * R + c0, r[t]);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < HC; ++i) {
+                    const float y = fmaf(0.125f, fmaf(0.125f, __uint_as_float(r[2][i]), __uint_as_float(r[1][i])), __uint_as_float(r[0][i]));
+                    po[i * kDc + 128 * c] = __float2half_rn(y * fr[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(__uint_as_float(r[i]) * fr[i]);
             }
             ptx::tc_fence_before();
             meet();   // the sums are read
@@ -1386,12 +1374,13 @@ cudaError_t launch_attn(const CUtensorMap& ml, const CUtensorMap& mr, const Src&
 
 }  // namespace
 
-// Rows per group: the smallest of 16, 32 and 64 that holds a sequence's rows, else 64 (the most
-// whose O and scores fit the tensor memory).  Against 64 for all: 16 heads 46.0 and 61.2 us, 32
-// heads 49.4 and 57.3 us (48 ragged sequences of up to 9001 tokens).
+// Rows per group: 16 where that holds a sequence's rows, else 32 (the most whose scores and O, three
+// terms each with its own accumulator, fit the tensor memory).  Groups of 64 rows, O in one
+// accumulator for two E4M3 terms, were quicker (128 heads, 32 x 4096 tokens: 60.9 us against 69.5), but
+// left nothing of a probability below 2^-11 of its tile's largest.
 Shape make_shape(int B, int q_len, int H, int num_sms) {
     const int rows = q_len * H;
-    Shape s{B, q_len, H, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 1, 1, num_sms};
+    Shape s{B, q_len, H, rows <= 16 ? 16 : 32, 1, 1, num_sms};
     s.G = (rows + s.R - 1) / s.R;
     s.sib = s.G <= kMaxSib && s.G <= num_sms ? s.G : 1;
     return s;
@@ -1442,9 +1431,7 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
         if (!make_tmap(&ml, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.codes, 2, dc, sc, bl, 128) ||
             !make_tmap(&mr, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.codes, 2, dc, sc, br, 64))
             return cudaErrorInvalidValue;
-        e = s.R == 16   ? launch_attn<16>(ml, mr, src, p, ws, err, st)
-            : s.R == 32 ? launch_attn<32>(ml, mr, src, p, ws, err, st)
-                        : launch_attn<64>(ml, mr, src, p, ws, err, st);
+        e = s.R == 16 ? launch_attn<16>(ml, mr, src, p, ws, err, st) : launch_attn<32>(ml, mr, src, p, ws, err, st);
         if (e != cudaSuccess) return e;
     }
     ProfScope ps(st, "q8_merge_w_uv");

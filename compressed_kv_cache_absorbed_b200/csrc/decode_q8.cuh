@@ -16,7 +16,7 @@ namespace q8 {
 // rows, and how many CTAs walk one sequence's tiles side by side.
 struct Shape {
     int B, q_len, H;
-    int R;        // rows per group: 16, 32 or 64
+    int R;        // rows per group: 16 or 32
     int G;        // groups per sequence
     int sib;      // > 1: the G groups of a sequence are walked by G neighbouring CTAs; 1: one after another
     int ctas;     // CTAs of the attention kernel

@@ -5,9 +5,9 @@ Tolerances.  Appended rows: the latent's bits; a rotated key is rounded once to 
 to storage, so it is within (half a bf16 step = 2^-8 relative) + 2^-23 of the exact rotation,
 fp32 storage within 2^-22.  Codes: within half an E4M3 step of value / scale, 2^-4 relative or,
 where E4M3 is subnormal (step 2^-9), 2^-10 absolute, + 2^-22 for the fp32 quotient's input.
-Decode: the library's bf16 tolerance (helpers.assert_close).  The kernel rounds queries and
-probabilities to two 8-bit terms each (at most 2^-8 and 2^-7 relative), which by the same
-count as bf16 operands (2^-8 each) is inside it."""
+Decode: the library's bf16 tolerance (helpers.assert_close).  The kernel rounds queries to two
+8-bit terms (at most 2^-8 relative, or 2^-17 of the row's largest value) and probabilities to three
+(2^-9), which by the same count as bf16 operands (2^-8 each) is inside it."""
 from __future__ import annotations
 
 import numpy as np
