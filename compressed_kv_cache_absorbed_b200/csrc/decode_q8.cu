@@ -36,8 +36,15 @@
 // is 2^-27 of it.  A new reference costs a wait for the O product before and a pass over O, so the
 // window is as wide as those bits allow and its set point leaves most of the room above, where new
 // maxima come: with scores of 3 nats' spread, 32 sequences of 4096 tokens, 128 heads, 74.9 us, and 84.0
-// with the window [2^4, 2^15.5] set at 2^10.  The pages' scales ride on the
-// probabilities: z' = z + log2(s_j / s_ref) with s_ref the piece's first page's scale.
+// with the window [2^4, 2^15.5] set at 2^10.
+//
+// The scales.  They ride on the probabilities: z' = z + log2(s_j / s_ref) with s_ref the piece's first
+// page's scale.  A page of large scale need not hold large values (a page of zeros has the scale 1,
+// one large value raises its whole page's), so no page's probabilities may cost another's bits: where
+// the two pages of a tile are more than 2^4 apart the tile is visited twice, each page's tokens alone,
+// and a visit whose scale is as far from the one before sets the references anew.  The output of a
+// piece with such pages leaves in fp16 against each row's largest value.  What remains is fp32's range:
+// O is rescaled by up to 2^kFarLog2 as the references go down.
 #include <math.h>
 
 #include <atomic>
@@ -67,7 +74,10 @@ constexpr int kMaxSib = 8;
 constexpr float kPGain = 1.f / 64;            // p = 2^-6 2^(z' - M)
 constexpr float kTopLog2 = 21.5f;             // p <= 2^15.5 (the largest E5M2 value is 1.75 x 2^15)
 constexpr float kSetLog2 = 10.f;              // a new reference puts the tile's largest p at 2^4
-constexpr float kFarLog2 = 64.f;              // how far below its highest value a reference may go
+// How far below its highest value a reference may go: O, at most 2^15.5 x 448 x 2^20 tokens, stays
+// below 2^127.  Scales 2^60 apart leave 2^20 of it to the scores.
+constexpr float kFarLog2 = 80.f;
+constexpr float kApart = 16.f;                // scales further apart than this do not share a visit
 
 // Shared memory: NC chunk slots (as many as fit), NR slots that hold a tile's rotary columns and
 // then its P (three terms of R bytes per token), the group's queries.
@@ -235,6 +245,11 @@ struct Src {
 __device__ __forceinline__ int tiles_of(int L) { return L > 0 ? (L + kT - 1) / kT : 0; }
 __device__ __forceinline__ long long cost_of(int n) { return n > 0 ? n + kPieceCost : 0; }
 
+// Marks of a visit: the same tile comes again, its first (second) page does not count, its scale is
+// far from the visit's before, the piece's scales so far are far apart
+constexpr int kAgain = 1, kNotFirst = 2, kNotSecond = 4, kJump = 8, kWide = 16;
+__device__ __forceinline__ int marks(const float4& visit) { return __float_as_int(visit.z); }
+
 // tiles [j0, j1) of group g of sequence b (j0 = j1: no more pieces)
 struct Seg {
     int b, item, g, j0, j1, len, kmin, kmax, slot, pad[3];
@@ -315,11 +330,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     uint64_t *seg_full = rope_full + 20, *seg_empty = rope_full + 22;
     Seg* segs = (Seg*)(rope_full + 24);                 // [2] the pieces of this CTA, from the planning warp
     uint32_t* flags = (uint32_t*)(segs + 2);            // [2 tiles][CG][4]
-    float* page_scale = (float*)(flags + 32);           // [4 tiles][2 pages]
-    float* out_scale = page_scale + 8;                  // [CG][4] largest page scale a warp saw
-    uint32_t* tmem_slot = (uint32_t*)(out_scale + 16);
+    float4* visit = (float4*)(flags + 32);              // [4 visits] scales of the tile's two pages, marks (kAgain ..), largest scale so far
+    uint32_t* tmem_slot = (uint32_t*)(visit + 4);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-    static_assert(32 * 4 + 64 * 16 + 64 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 8 + 16 + 2) * 4 <= C::kMisc, "barrier area");
+    static_assert(32 * 4 + 64 * 16 + 64 * 4 + (2 * NC + 24) * 8 + 2 * sizeof(Seg) + (32 + 16 + 2) * 4 <= C::kMisc, "barrier area");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NC; ++i) {
@@ -390,16 +404,18 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         // lane l holds the page (and its scale) of block base + l of the sequence
         const uint64_t policy = src.s.G > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
         const long long none = num_pages * kPageRows;   // a box past the last row reads zeros
-        uint32_t g = 0, cn = 0, slot = 0, use = 0;      // tiles and chunks requested, next slot and its uses
+        uint32_t g = 0, cn = 0, slot = 0, use = 0;      // visits and chunks requested, next slot and its uses
         bool ok = true;
         while (ok && next_piece()) {
             const int blocks = (sg.len + kPageRows - 1) / kPageRows;
             long long row = none;
             float sc = 0.f;
+            int mark = 0;
+            float s_ref = 0.f, s_last = 0.f, s_hi = 0.f, s_lo = INFINITY;   // scales: the first visit's (0: none yet), the one's before, extremes
 #pragma unroll 1
-            for (int j = sg.j0; ok && j < sg.j1; ++j) {
+            for (int j = sg.j0; ok && j < sg.j1; j += !(mark & kAgain)) {
                 const int at = (j - sg.j0) & 15;
-                if (at == 0) {
+                if (at == 0 && !(mark & kAgain)) {
                     const int blk = 2 * j + lane;
                     const long long page = blk < blocks ? block_table[(long long)sg.b * src.max_blocks + blk] : -1;
                     const bool good = page >= 0 && page < num_pages;
@@ -422,11 +438,27 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     if (++slot == NC) slot = 0, ++use;
                 }
                 // the scales may still be on their way here, which must not hold up the loads above
-                const float s0 = __shfl_sync(0xffffffffu, sc, 2 * at), s1 = __shfl_sync(0xffffffffu, sc, 2 * at + 1);
+                float s0 = __shfl_sync(0xffffffffu, sc, 2 * at), s1 = __shfl_sync(0xffffffffu, sc, 2 * at + 1);
                 if (ok && g >= NR && !wait_warp(&rope_empty[g % NR], (g / NR - 1) & 1, abort_flag)) ok = false;
+                if (mark & kAgain)
+                    mark = kNotFirst;
+                else
+                    mark = s0 > 0.f && s1 > 0.f && (s0 > kApart * s1 || s1 > kApart * s0) ? kAgain | kNotSecond : 0;
+                // the visit's scale (0: neither page is in the cache)
+                const float s_now = mark & kNotFirst ? s1 : mark & kNotSecond ? s0 : fmaxf(s0, s1);
+                if (j == sg.j0 && !(mark & kNotFirst)) s_ref = s_last = s_now > 0.f ? s_now : 1.f;
+                if (s_now > 0.f) {
+                    if (s_now > kApart * s_last || s_last > kApart * s_now) mark |= kJump;
+                    s_last = s_now;
+                }
+                s_hi = fmaxf(s_hi, s_last);
+                s_lo = fminf(s_lo, s_last);
+                if (s_hi > kApart * s_lo) mark |= kWide;
+                // no page: zero rows; the softmax need not look at the scale of what does not count
+                if (s0 == 0.f || (mark & kNotFirst)) s0 = s_ref;
+                if (s1 == 0.f || (mark & kNotSecond)) s1 = s_ref;
                 if (ok && elect()) {
-                    page_scale[2 * (g & 3)] = s0;
-                    page_scale[2 * (g & 3) + 1] = s1;
+                    visit[g & 3] = make_float4(s0, s1, __int_as_float(mark), s_hi);
                     uint8_t* dst = ropes + (g % NR) * C::kSlotBytes;
                     ptx::mbar_expect_tx(&rope_full[g % NR], kRopeBytes);
                     ptx::tma_load_2d_hint(dst, &tm_rope, &rope_full[g % NR], kDc, r0, policy);
@@ -471,7 +503,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(q_full, piece & 1, nullptr))) { ok = false; break; }
             ++piece;
 #pragma unroll 1
-            for (int left = uniform(sg.j1 - sg.j0); left > 0; --left, ++g) {
+            for (int left = uniform(sg.j1 - sg.j0); left > 0; ++g) {
                 if (g >= 2 && !wait(&s_free[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
                 const uint32_t d = tmem + (g & 1) * (2 * R);
 #pragma unroll
@@ -493,6 +525,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     for (int k = 0; k < 2; ++k) mma_f8(d, a + 2 * k, h64, b + 2 * k, h64, idesc, 1);
                     ptx::mma_commit(&s_full[g & 1]);
                 }
+                left -= uniform(!(marks(visit[g & 3]) & kAgain));
             }
         }
         if (!ok) fail(err, abort_flag, 12);
@@ -509,7 +542,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         while (ok && next_piece()) {
             uint32_t acc0 = 0;
 #pragma unroll 1
-            for (int left = uniform(sg.j1 - sg.j0); left > 0; --left, ++g) {
+            for (int left = uniform(sg.j1 - sg.j0); left > 0; ++g) {
                 if (!wait_warp(&p_ready[g & 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t p = p0 + (g % NR) * (C::kSlotBytes >> 4);
@@ -530,6 +563,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 }
                 slot0 = (slot0 + 4) % NC;
                 acc0 = 1;
+                left -= uniform(!(marks(visit[g & 3]) & kAgain));
             }
         }
         if (!ok) fail(err, abort_flag, 16);
@@ -554,19 +588,22 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         f32x2 l[HC / 2];           // this thread's share of each row's sum
         float m_row = 0.f, m_top = 0.f;   // lane i: reference of row c0 + i, and the highest it has had
         while (ok && next_piece()) {
-            float s_ref = 1.f, s_top = 0.f;
+            float s_ref = 1.f, s_hi = 1.f;   // the first visit's scale and the largest so far
+            bool first = true;
+            int mark = 0;
 #pragma unroll 1
-            for (int j = sg.j0; j < sg.j1; ++j, ++g) {
-                const bool first = j == sg.j0;
+            for (int j = sg.j0; j < sg.j1; j += !(mark & kAgain), ++g, first = false) {
                 if (first && !uwait(q_full, piece & 1)) { ok = false; break; }   // row scales
                 if (!uwait(&rope_full[g % NR], (g / NR) & 1)) { ok = false; break; }   // page scales
                 // O of tile g - 2 is done, whose P lay where this tile's goes.  Every phase of a
                 // barrier is waited for, so that a later wait cannot take an older one for its own.
                 if (g >= 2 && !uwait(&o_done[g & 1], ((g >> 1) - 1) & 1)) { ok = false; break; }
-                float s = page_scale[2 * (g & 3) + (quad >> 1)];
+                const float4 vi = visit[g & 3];
+                mark = marks(vi);
+                s_hi = vi.w;
+                const float s = quad < 2 ? vi.x : vi.y;
                 if (first) {
-                    const float sa = page_scale[2 * (g & 3)], sb = page_scale[2 * (g & 3) + 1];
-                    s_ref = sa != 0.f ? sa : sb != 0.f ? sb : 1.f;
+                    s_ref = vi.w;
 #pragma unroll
                     for (int i = 0; i < HC / 2; ++i) l[i] = 0;
                     m_row = 0.f;
@@ -576,8 +613,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     }
                     __syncwarp();
                 }
-                s_top = fmaxf(s_top, s);
-                if (s == 0.f) s = s_ref;   // no page: zero rows
                 const bool same = s == s_ref;
                 const float back = same ? 1.f : s_ref / s;
                 if (!uwait(&s_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
@@ -609,9 +644,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     }
                 }
                 ptx::mbar_arrive(&s_free[g & 1]);   // also done with the row scales
-                const bool edge = (j + 1) * kT > sg.kmin;   // some row does not see the whole tile
+                // some row does not see the whole tile, or a page does not count
+                const bool edge = (j + 1) * kT > sg.kmin || (mark & (kNotFirst | kNotSecond));
                 if (edge) {
-                    const int at = j * kT + tok;
+                    const int at = mark & (quad < 2 ? kNotFirst : kNotSecond) ? 0x7fffffff : j * kT + tok;
                     if (sg.kmin == sg.kmax) {
                         if (at >= sg.kmax) {
 #pragma unroll
@@ -655,7 +691,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 if (!ok) break;
                 const uint4 fl = *(const uint4*)(flags + ((g & 1) * CG + grp) * 4);
                 const bool over = fl.x == 0xffffffffu || fl.y == 0xffffffffu || fl.z == 0xffffffffu || fl.w == 0xffffffffu;
-                if (first || over || (fl.x & fl.y & fl.z & fl.w) != 0) {
+                if (first || (mark & kJump) || over || (fl.x & fl.y & fl.z & fl.w) != 0) {
                     // this warp's largest argument of each row, then the tile's, row i in lane i
                     float keep = -INFINITY;
 #pragma unroll
@@ -674,7 +710,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     if (lane < HC) {
                         const float4 v = red[grp * 16 + lane];
                         const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                        if (mx > -INFINITY && (first || mx > kTopLog2 || mx < 0.f)) {
+                        if (mx > -INFINITY && (first || (mark & kJump) || mx > kTopLog2 || mx < 0.f)) {
                             step = mx - kSetLog2;
                             if (!first) step = fmaxf(step, m_top - kFarLog2 - m_row);
                         }
@@ -785,25 +821,69 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                     ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], o);
                 }
             }
+            auto o_ready = [&]() {
+                if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) ok = false;
+                ptx::tc_fence_after();
+            };
+            // latents 128 c + tok of O
+            auto load_o = [&](int c, float (&y)[HC]) {
+                uint32_t r[C::kTerms][HC];
+#pragma unroll
+                for (int t = 0; t < C::kTerms; ++t) tmem_ld(lane_addr + C::kColO + c * C::NP + t * R + c0, r[t]);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < HC; ++i)
+                    y[i] = fmaf(0.125f, fmaf(0.125f, __uint_as_float(r[2][i]), __uint_as_float(r[1][i])), __uint_as_float(r[0][i]));
+            };
+            // Lane i: row c0 + i leaves as fp16 values f O, with a unit of its own.  Pages of about one scale:
+            // 64 x the mean code (at most 448 each, so <= 28672, and down to 2^-20 with all bits), in
+            // units of the largest scale.  Pages of very different scales: against the row's largest
+            // |O|, which takes another pass over it (a row under 2^-100 counts as zero).
+            const bool wide = mark & kWide;
+            float keep = 0.f;                         // lane i: the largest |O| of row c0 + i this warp has
+            if (wide) {
+                o_ready();
+                if (!ok) break;
+                float most[HC];
+#pragma unroll
+                for (int i = 0; i < HC; ++i) most[i] = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float y[HC];
+                    load_o(c, y);
+#pragma unroll
+                    for (int i = 0; i < HC; ++i) most[i] = fmaxf(most[i], fabsf(y[i]));
+                }
+#pragma unroll
+                for (int i = 0; i < HC; ++i) {
+                    const float m = warp_max(most[i]);
+                    if (lane == i) keep = m;
+                }
+            }
             // row held by this lane: the lane bits from 16 down, as many as HC has
             const int my_row = lane >> 2;
-            float* sums = (float*)(red + grp * 16);   // [4 quarters][16]
+            float* sums = (float*)(red + grp * 16);   // [4 quarters][8 sums, 8 largest |O|]
             meet();   // red is read
             if (!ok) break;
             sums[quad * 16 + my_row] = ls[0];
-            if (lane == 0) out_scale[grp * 4 + quad] = s_top;
+            if (lane < HC) sums[quad * 16 + 8 + lane] = keep;
             meet();
+            o_ready();
             if (!ok) break;
-            const float* st4 = out_scale + grp * 4;
-            const float s_out0 = fmaxf(fmaxf(st4[0], st4[1]), fmaxf(st4[2], st4[3]));
-            const float s_out = s_out0 > 0.f ? s_out0 : 1.f;
-            if (!uwait(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) { ok = false; break; }
-            ptx::tc_fence_after();
-            float f = 0.f;   // lane i: what turns row c0 + i of O into its normalised output
+            float f = 0.f;
             if (lane < HC) {
                 const float t = (sums[lane] + sums[16 + lane]) + (sums[32 + lane] + sums[48 + lane]);
-                f = t != 0.f ? (s_ref / s_out) / (kPGain * t) : 0.f;
-                if (quad == 0) ws.part_ml[(size_t)sg.slot * R + c0 + lane] = make_float4(m_row, t, s_out, 0.f);
+                const float mean = t != 0.f ? s_ref / (kPGain * t) : 0.f;   // times O: the row's values
+                float unit;
+                if (wide) {
+                    const float top = fmaxf(fmaxf(sums[8 + lane], sums[24 + lane]), fmaxf(sums[40 + lane], sums[56 + lane]));
+                    f = top >= 0x1p-100f ? 0x1p14f / top : 0.f;
+                    unit = mean * (top * 0x1p-14f);
+                } else {
+                    unit = s_hi * 0x1p-6f;
+                    f = mean / unit;
+                }
+                if (quad == 0) ws.part_ml[(size_t)sg.slot * R + c0 + lane] = make_float4(m_row, t, unit, 0.f);
             }
             // (a warp's store is 64 contiguous bytes; turning the tile around with shuffles for
             // 16-byte stores took longer)
@@ -813,15 +893,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
             for (int i = 0; i < HC; ++i) fr[i] = __shfl_sync(0xffffffffu, f, i);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t r[C::kTerms][HC];
+                float y[HC];
+                load_o(c, y);
 #pragma unroll
-                for (int t = 0; t < C::kTerms; ++t) tmem_ld(lane_addr + C::kColO + c * C::NP + t * R + c0, r[t]);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < HC; ++i) {
-                    const float y = fmaf(0.125f, fmaf(0.125f, __uint_as_float(r[2][i]), __uint_as_float(r[1][i])), __uint_as_float(r[0][i]));
-                    po[i * kDc + 128 * c] = __float2half_rn(y * fr[i]);
-                }
+                for (int i = 0; i < HC; ++i) po[i * kDc + 128 * c] = __float2half_rn(y[i] * fr[i]);
             }
             ptx::tc_fence_before();
             meet();   // the sums are read
@@ -1123,8 +1198,8 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
 // ------------------------------------------------------------- merge and W_UV
 // out[v, h, :] = W_UV[h] o_lat[v, h, :],
-// o_lat = sum_p 2^(m_p - m) l_p s_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
-// piece's normalised output in units of s_p.  One CTA per (head, `per` queries), per = 32, or 16
+// o_lat = sum_p 2^(m_p - m) l_p u_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
+// piece's output in units of u_p.  One CTA per (head, `per` queries), per = 32, or 16
 // or 8 where that still is one wave of CTAs (48 sequences, 16 heads: 43.2 -> 41.1 us).  W_UV[h]
 // comes by TMA before the wait for the attention kernel; sixteen warps merge the rows into the B
 // operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), rows r and 32 + r,

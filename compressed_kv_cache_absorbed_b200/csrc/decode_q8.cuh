@@ -27,8 +27,8 @@ Shape make_shape(int B, int q_len, int H, int num_sms);
 struct Ws {
     uint8_t* q_img;     // [B G][2 R rows x 576]: the queries as 8-bit operands
     float* q_scale;     // [B G][R]
-    __half* part_o;     // [slots][R][512] normalised partial outputs
-    float4* part_ml;    // [slots][R] (reference, sum, scale of the output, -)
+    __half* part_o;     // [slots][R][512] partial outputs, each row in units of its own
+    float4* part_ml;    // [slots][R] (reference, sum, unit of the output, -)
     int4* start;        // [ctas]: where each range of the work split starts
     int2* pieces;       // [B G]: slots and number of each item's partials
     size_t bytes;

@@ -372,8 +372,9 @@ size_t mla_decode_q8_workspace_size(const mla_dims* dims, int32_t B, int32_t q_l
  * Any head count up to 128 (a head-parallel layer's share of the heads), bf16, d_c = 512,
  * d_hR = 64, qk_nope = v_head = 128, handles without W_O, B * q_len <= 65535 and caches of
  * fewer than 2^31 rows, else MLA_ERR_UNSUPPORTED.  The
- * scales of the pages in use must be positive and finite (any such value, not only powers of
- * two).  What the pages hold behind a sequence's last token does not matter, NaN codes
+ * scales of the pages in use must be positive and finite (not only powers of two), within
+ * 2^60 of one another in a sequence; a page's share of the output keeps its precision beside
+ * pages of any larger or smaller scale.  What the pages hold behind a sequence's last token does not matter, NaN codes
  * included.  A token with no key gets zeros.  A sequence with a negative length or more than
  * max_blocks pages latches MLA_ERR_OUT_OF_RANGE and decodes to zeros; a page outside
  * [0, num_pages) latches the same error and its tokens are taken as zero rows.

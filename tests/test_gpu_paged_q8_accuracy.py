@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from helpers import assert_close
-from test_gpu_paged_q8 import DC, DEV, E4M3, PAGE, ROW, SCALE, Decode, gen, mla
+from test_gpu_paged_q8 import DC, DEV, DR, E4M3, PAGE, ROW, SCALE, Decode, gen, mla
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,78 @@ def test_spread_scores(H, sigma, peak):
     at = i % 120 == 0
     set_scores(D, peak * at.float() + sigma * torch.randn(n, generator=gen(9), device=DEV), at, noise=0.2)
     D.check(f"H={H} sigma {sigma} nats, peaks of {peak}")
+
+
+# Pages of one sequence whose scales differ, as appends make them: a page of zeros gets the scale 1,
+# one large value raises its whole page's.  The formula weighs each value by its own page's scale, so
+# every page's share of the output has to keep its precision beside any other's scale.
+
+def filled(H, Q, rows, seed, qgain, dead_column=None):
+    """A decode over one sequence whose pages mla_append_paged_q8 made from rows [n, 576]."""
+    n = len(rows)
+    D = Decode(H, Q, [n], seed=seed, qgain=qgain)
+    if dead_column is not None:              # a latent that neither scores nor outputs use
+        D.uk[..., dead_column] = 0
+        D.uv[..., dead_column] = 0
+        D.w = mla.mla_absorb_weights(D.d, D.uk, D.uv)
+    rows = rows.to(torch.bfloat16)
+    zero = torch.zeros(n, DR, dtype=torch.bfloat16, device=DEV)
+    mla.mla_append_paged_q8(D.d, rows[:, :DC].contiguous(), zero, torch.tensor([0, n], dtype=torch.int32, device=DEV),
+                            D.lens, D.codes, D.scales, D.table)
+    return D
+
+
+@pytest.mark.parametrize("H,Q", [(16, 1), (128, 1), (24, 3)])
+@pytest.mark.parametrize("size", [0.1, 1e-2, 1e-3, 1e-6, 1e-15])
+@pytest.mark.parametrize("zeros", ["first page", "second page", "first tile", "every other", "last"])
+def test_pages_of_zeros_beside_small_latents(H, Q, size, zeros):
+    n, g = 700, gen(81)
+    mean = torch.randn(ROW, generator=g, device=DEV)
+    rows = size * (mean + 0.5 * torch.randn(n, ROW, generator=g, device=DEV))
+    page = torch.arange(n, device=DEV) // PAGE
+    rows[{"first page": page == 0, "second page": page == 1, "first tile": page < 2, "every other": page % 2 == 0,
+          "last": page == (n - 1) // PAGE}[zeros]] = 0
+    D = filled(H, Q, rows, 82, min(0.3 / size, 1e15))
+    assert float(D.scales[D.table[0].long()].amax()) == 1.0
+    D.check(f"H={H} q_len={Q} zeros: {zeros}, others {size}")
+
+
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("ratio", [2 ** 5, 2 ** 8, 2 ** 10, 2 ** 12, 2 ** 20])
+@pytest.mark.parametrize("where", ["every other", "first", "last"])
+def test_a_large_value_in_some_pages(H, ratio, where):
+    n, g = 1000, gen(83)
+    rows = torch.randn(ROW, generator=g, device=DEV) + 0.5 * torch.randn(n, ROW, generator=g, device=DEV)
+    page = torch.arange(n, device=DEV) // PAGE
+    hit = {"every other": page % 2 == 1, "first": page == 0, "last": page == (n - 1) // PAGE}[where]
+    rows[hit & (torch.arange(n, device=DEV) % PAGE == 7), 5] = 3.0 * ratio
+    filled(H, 1, rows, 84, 0.3, dead_column=5).check(f"H={H} ratio {ratio} {where}")
+
+
+@pytest.mark.parametrize("H,Q", [(16, 1), (128, 1), (64, 3)])
+@pytest.mark.parametrize("exps", [(0, 25), (-30, 30, 0), (5, 0, 0, -5, -11, -11), (0, 0, 0, -60), (0.4, 5.3), (4, 0), (0, 5)])
+def test_scales_of_any_ratio(H, Q, exps):
+    """Full-range pages times any scales: those of the largest make up the output."""
+    lens = [1200, 64, 130, 65, 128]
+    Decode(H, Q, lens, seed=85, exps=exps, qgain=2.0 ** -max(max(exps), 0)).check(f"H={H} q_len={Q} exps={exps}")
+
+
+def test_nan_behind_the_end_of_a_tile_of_two_scales():
+    for n in (100, 65, 64):
+        D = Decode(32, 1, [n], seed=86, exps=(0, 9), qgain=2.0 ** -9)
+        want = D.check(f"{n} tokens")
+        last = int(D.table[0, (n - 1) // PAGE])
+        if n % PAGE:
+            D.codes[last, n % PAGE:] = 0xFF
+        assert torch.equal(D.check(f"{n} tokens, NaN behind them"), want)
+
+
+def test_bad_page_beside_a_page_of_another_scale():
+    D = Decode(16, 1, [500], seed=87, exps=(0, 12, -3), qgain=2.0 ** -12)
+    keep = int(D.table[0, 3])
+    D.table[0, 3] = -1
+    out = D.run()
+    assert mla.mla_get_device_error()[0] == mla.MLA_ERR_OUT_OF_RANGE
+    D.table[0, 3] = keep
+    D.codes[keep] = 0
+    assert_close(out.float(), D.plain(), "bf16", "bad page")
