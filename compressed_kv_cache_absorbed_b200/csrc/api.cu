@@ -291,6 +291,8 @@ extern "C" mla_status mla_absorb_weights(const mla_dims* d, const void* W_UK, co
             return MLA_ERR_NO_MEMORY;
         }
     }
+    // the decodes' first kernels load the packed weights before they wait for earlier kernels
+    if (e == cudaSuccess) e = mla::launch_order(s);
     if (e != cudaSuccess) {
         cudaStreamSynchronize(s);
         free_weights(w);

@@ -132,4 +132,10 @@ template <typename T>
 cudaError_t launch_transpose_heads(const T* src, T* dst, int Hn, int R, int C, cudaStream_t s,
                                    long long src_head_stride = -1);
 
+// A kernel that does nothing, between what a call wrote and kernels of later calls that read it
+// before their pdl_wait(): launched plainly it starts when all earlier work of the stream is
+// complete, so a kernel launched with launch_pdl behind it finds that work done from its first
+// instruction on.
+cudaError_t launch_order(cudaStream_t s);
+
 }  // namespace mla

@@ -1058,7 +1058,7 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         ptx::mbar_init(d_full, 1);
         ptx::fence_mbar_init();
         ptx::mbar_expect_tx(full, kAbsorbA + kAbsorbB);
-        // the weights first: earlier kernels do not write them
+        // the weights first: the call that packed them ended with a kernel of its own (launch_order)
 #pragma unroll
         for (int kc = 0; kc < 2; ++kc) ptx::tma_load_2d(sB + kc * 32768, &tm_w, full, 64 * kc, h * kDc + 256 * rank);
         pdl_wait();      // all earlier work is done

@@ -995,7 +995,7 @@ merge_wuv_kernel(const __nv_bfloat16* __restrict__ uv, const SeqSrc src, int P, 
         ptx::mbar_init(d_full, 1);
         ptx::fence_mbar_init();
         if (!kLat) {
-            // the weights are not written by earlier kernels: load them before waiting; the
+            // the call that packed the weights ended with launch_order: load them before waiting; the
             // tiled copy is already the shared-memory image, 8 contiguous 16 KB chunks per head
             ptx::mbar_expect_tx(a_full, kMergeABytes);
             const uint8_t* src = (const uint8_t*)uv + (size_t)h * kMergeABytes;
@@ -1333,7 +1333,7 @@ absorb_q_kernel(const __nv_bfloat16* __restrict__ ukt, const __grid_constant__ C
         ptx::fence_mbar_init();
         ptx::tma_prefetch(&tm_q);
         ptx::mbar_expect_tx(full, 2 * kAbsorbTiles * 16384 + 2 * BN * 128);
-        // weights first (earlier kernels do not write them): the tiled copy is already the
+        // weights first (the call that packed them ended with launch_order): the tiled copy is already the
         // shared-memory image, chunk (t, k) at (2t + k) x 16 KB; this CTA takes tiles t0 ..
         const uint8_t* src = (const uint8_t*)ukt + ((size_t)h * 8 + 2 * t0) * 16384;
 #pragma unroll

@@ -105,7 +105,7 @@ int32_t mla_decode_path(const mla_dims* dims);
  * W_Q rows are head-major, the qk_nope content rows of a head before its d_hR rotary rows.
  * Borrowed tensors must stay valid until mla_weights_destroy.  The handle owns device
  * memory allocated here (the only allocation the library makes).  Stream-ordered: the
- * packing kernels run on `stream`.
+ * packing kernels run on `stream`, and a call that uses the handle may follow directly.
  *
  * fold = 1 also precomputes the matrix products the up-projections can be folded into
  * [L1 "Coste de computo": precomputed products], per head h (fp32 sums, one rounding; W_QUK
