@@ -95,7 +95,9 @@ __device__ __forceinline__ bool mbar_try_cluster(uint64_t* bar, uint32_t parity)
 // hardware-defined interval), then returns false so the caller can record a timeout and
 // leave instead of hanging the GPU.  The limit is a device variable so that a test can
 // shorten it (mla_set_wait_limit); every file that includes this header has its own copy,
-// which set_wait_limit_of_this_file() sets on the current device.
+// which set_wait_limit_of_this_file() sets on the current device.  A wait without an abort flag
+// is one for copies or products that this CTA has itself under way: they end without anyone's help and must
+// have before its shared or tensor memory is given up, so it keeps the default limit.
 constexpr uint32_t kDefaultWaitLimit = 1u << 22;
 static __constant__ uint32_t g_wait_limit = kDefaultWaitLimit;   // constant bank: read as an operand
 
@@ -105,7 +107,7 @@ static inline cudaError_t set_wait_limit_of_this_file(uint32_t polls) {
 
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
     if (mbar_try(bar, parity)) return true;   // the common case reads no limit
-    const uint32_t limit = g_wait_limit;
+    const uint32_t limit = abort_flag ? g_wait_limit : kDefaultWaitLimit;
     for (uint32_t i = 1; i < limit; ++i) {
         if (abort_flag && *abort_flag) return false;
         if (mbar_try(bar, parity)) return true;

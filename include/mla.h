@@ -427,13 +427,14 @@ mla_status mla_rope_apply(const float* x, const double* cos_sin, int64_t pairs, 
  * mla_set_wait_limit: on the current device, the number of polls each bounded wait in the
  * library's tensor-core kernels (a kernel waiting for its own loads, MMAs or sibling warps)
  * makes before it gives up, latches MLA_ERR_DEVICE_TIMEOUT, drains what it issued, frees its
- * tensor memory and returns.  0 restores the default (2^22 polls, seconds).  Synchronous
- * (cudaMemcpyToSymbol); call it with no library kernel running.
+ * tensor memory and returns.  0 restores the default (2^22 polls, seconds).  A kernel's wait
+ * for its own copies and products that are already under way, the drain among them, keeps the
+ * default.  Synchronous (cudaMemcpyToSymbol); call it with no library kernel running.
  *
  * mla_test_starve_projection: while on != 0, the loader warp of the tensor-core projection
  * GEMM (the kernel behind mla_append_cache on bf16, the query projection and W_O) issues no
  * loads, so its MMA and epilogue waits run out: such a call writes no output and latches
- * MLA_ERR_DEVICE_TIMEOUT, with no copy and no MMA in flight, and the next call works.  It is
+ * MLA_ERR_DEVICE_TIMEOUT, with no copy and no MMA in flight, and the next call works.   It is
  * how the timeout path is tested without faulting or hanging the GPU.  Current device,
  * synchronous. */
 mla_status mla_set_wait_limit(uint32_t polls);
