@@ -427,7 +427,8 @@ def mla_set_wait_limit(polls: int) -> None:
 
 
 def mla_test_starve_projection(on: bool) -> None:
-    """While on, the projection GEMM's loader issues no loads so its waits run out (test hook)."""
+    """While on, the projection GEMM's loader issues no loads, and the 8-bit paged decode's none of the
+    rotary columns, so that their waits run out (test hook)."""
     _check(_lib.mla_test_starve_projection(1 if on else 0), "mla_test_starve_projection")
 
 

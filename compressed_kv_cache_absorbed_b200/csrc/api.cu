@@ -1055,6 +1055,7 @@ extern "C" mla_status mla_set_wait_limit(uint32_t polls) {
 
 extern "C" mla_status mla_test_starve_projection(int32_t on) {
     MLA_CUDA(mla::tc::set_starve_gemm(on ? 1 : 0));
+    MLA_CUDA(mla::q8::set_starve_decode_q8(on ? 1 : 0));
     return MLA_OK;
 }
 

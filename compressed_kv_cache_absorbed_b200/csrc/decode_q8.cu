@@ -298,6 +298,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
     return false;
 }
 
+// Test hook (mla_test_starve_projection): nonzero = the attention's loader asks for the latents but
+// not for the rotary columns, so that the waits behind them run out with copies under way.
+__device__ int g_starve_loads = 0;
+
 __device__ __noinline__ void fail(DevErr err, volatile int* abort_flag, int where) {
     latch(err, kErrTimeout, (long long)where * 1000000 + blockIdx.x);
     *abort_flag = 1;
@@ -376,7 +380,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
     uint32_t segs_seen = 0;
     auto next_piece = [&]() -> bool {
         const uint32_t k = segs_seen & 1;
-        if (!wait_warp(&seg_full[k], (segs_seen >> 1) & 1, abort_flag)) return false;
+        if (!wait_warp(&seg_full[k], (segs_seen >> 1) & 1, abort_flag)) {
+            fail(err, abort_flag, 10);
+            return false;
+        }
         sg = segs[k];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&seg_empty[k]);
@@ -391,7 +398,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
 #pragma unroll 1
         for (uint32_t n = 0; more; ++n) {
             more = it.next(sg);
-            if (n >= 2 && !wait_warp(&seg_empty[n & 1], ((n >> 1) - 1) & 1, abort_flag)) break;
+            if (n >= 2 && !wait_warp(&seg_empty[n & 1], ((n >> 1) - 1) & 1, abort_flag)) {
+                fail(err, abort_flag, 15);
+                break;
+            }
             if (!more) sg.j0 = sg.j1 = 0;
             if (lane == 0) {
                 segs[n & 1] = sg;
@@ -405,6 +415,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
         const uint64_t policy = src.s.G > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
         const long long none = num_pages * kPageRows;   // a box past the last row reads zeros
         uint32_t g = 0, cn = 0, slot = 0, use = 0;      // visits and chunks requested, next slot and its uses
+        const bool starve = g_starve_loads;
         bool ok = true;
         while (ok && next_piece()) {
             const int blocks = (sg.len + kPageRows - 1) / kPageRows;
@@ -457,14 +468,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ 
                 // no page: zero rows; the softmax need not look at the scale of what does not count
                 if (s0 == 0.f || (mark & kNotFirst)) s0 = s_ref;
                 if (s1 == 0.f || (mark & kNotSecond)) s1 = s_ref;
-                if (ok && elect()) {
+                if (ok && !starve && elect()) {
                     visit[g & 3] = make_float4(s0, s1, __int_as_float(mark), s_hi);
                     uint8_t* dst = ropes + (g % NR) * C::kSlotBytes;
                     ptx::mbar_expect_tx(&rope_full[g % NR], kRopeBytes);
                     ptx::tma_load_2d_hint(dst, &tm_rope, &rope_full[g % NR], kDc, r0, policy);
                     ptx::tma_load_2d_hint(dst + kRopeBytes / 2, &tm_rope, &rope_full[g % NR], kDc, r1, policy);
                 }
-                g += ok;
+                g += ok && !starve;
             }
         }
         if (!ok) fail(err, abort_flag, 11);
@@ -1522,6 +1533,7 @@ cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, c
 }
 
 cudaError_t set_wait_limit_decode_q8(uint32_t polls) { return ptx::set_wait_limit_of_this_file(polls); }
+cudaError_t set_starve_decode_q8(int on) { return cudaMemcpyToSymbol(g_starve_loads, &on, sizeof on); }
 
 }  // namespace q8
 }  // namespace mla

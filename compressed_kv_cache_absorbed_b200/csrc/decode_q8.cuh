@@ -52,6 +52,7 @@ struct Problem {
 cudaError_t decode(const Problem& p, const Shape& s, const Ws& ws, DevErr err, cudaStream_t st);
 
 cudaError_t set_wait_limit_decode_q8(uint32_t polls);
+cudaError_t set_starve_decode_q8(int on);
 
 }  // namespace q8
 }  // namespace mla

@@ -434,9 +434,10 @@ mla_status mla_rope_apply(const float* x, const double* cos_sin, int64_t pairs, 
  * mla_test_starve_projection: while on != 0, the loader warp of the tensor-core projection
  * GEMM (the kernel behind mla_append_cache on bf16, the query projection and W_O) issues no
  * loads, so its MMA and epilogue waits run out: such a call writes no output and latches
- * MLA_ERR_DEVICE_TIMEOUT, with no copy and no MMA in flight, and the next call works.   It is
- * how the timeout path is tested without faulting or hanging the GPU.  Current device,
- * synchronous. */
+ * MLA_ERR_DEVICE_TIMEOUT, with no copy and no MMA in flight, and the next call works.  The loader of
+ * mla_decode_absorbed_paged_q8's attention asks for the latents but not for the rotary columns
+ * meanwhile: such a call latches the same error and leaves `out` undefined.  It is how the
+ * timeout path is tested without faulting or hanging the GPU.  Current device, synchronous. */
 mla_status mla_set_wait_limit(uint32_t polls);
 mla_status mla_test_starve_projection(int32_t on);
 
