@@ -335,11 +335,13 @@ mla_status mla_decode_absorbed_fp8(const mla_dims* dims, mla_weights w, const vo
  * device latch MLA_ERR_OUT_OF_RANGE: offsets that are negative, decreasing, or do not cover
  * exactly 0 .. n (nothing is written), a sequence with fewer tokens than new ones or more
  * than max_blocks pages (skipped), a page outside [0, num_pages) (its rows are skipped).
- * n = 0 is a no-op. */
+ * n = 0 is a no-op.  Every page's block looks through all B lengths: up to 64 sequences that costs
+ * nothing, a step of 1024 takes 16 us and one of 4096 110 us. */
 
-/* Into pages of the storage type: cache [num_pages, 64, d_c + d_hR], as
- * mla_decode_absorbed_paged and mla_decode_absorbed_paged_multi read it (fp32 or bf16; every
- * width the library supports). */
+/* Into pages of the storage type: cache [num_pages, 64, d_c + d_hR], fp32 or bf16, every width
+ * the library supports.  mla_decode_absorbed_paged and mla_decode_absorbed_paged_multi read
+ * such pages in bf16 with H = 128, d_c = 512, d_hR = 64 only; pages of other types and widths
+ * have no decode in this library. */
 mla_status mla_append_paged(const mla_dims* dims, const void* c, int64_t ld_c, const void* k_r, int64_t ld_kr,
                             const int32_t* new_offsets, const int32_t* seq_lens, const int32_t* pos, int32_t B,
                             int32_t n, void* cache, int64_t num_pages, const int32_t* block_table,
@@ -374,8 +376,12 @@ size_t mla_decode_q8_workspace_size(const mla_dims* dims, int32_t B, int32_t q_l
  * fewer than 2^31 rows, else MLA_ERR_UNSUPPORTED.  The
  * scales of the pages in use must be positive and finite (not only powers of two), within
  * 2^60 of one another in a sequence; a page's share of the output keeps its precision beside
- * pages of any larger or smaller scale.  What the pages hold behind a sequence's last token does not matter, NaN codes
- * included.  A token with no key gets zeros.  A sequence with a negative length or more than
+ * pages of any larger or smaller scale.
+ * Accuracy: codes are used as they are; W_UK^T q_nope and q_rope are held to 2^-8 of each value (2^-17
+ * of the row's largest where that is more), probabilities to 2^-9 of each down to 2^-18 of the
+ * row's largest (the least step is 2^-27 of it); sums and outputs are fp32 until each piece's
+ * latent output is rounded to fp16 against the row's size, and out to bf16.
+ * What the pages hold behind a sequence's last token does not matter, NaN codes included.  A token with no key gets zeros.  A sequence with a negative length or more than
  * max_blocks pages latches MLA_ERR_OUT_OF_RANGE and decodes to zeros; a page outside
  * [0, num_pages) latches the same error and its tokens are taken as zero rows.
  * Results do not depend on the order of execution: equal calls give equal bits.
