@@ -353,7 +353,8 @@ mla_status mla_append_paged(const mla_dims* dims, const void* c, int64_t ld_c, c
  * of two s with amax <= 448 s, amax over the finite new values of the page (1 if they are all
  * zero; at least 2^-60).  On a page that holds earlier tokens it never shrinks, and when it
  * grows their codes are re-expressed under it, exactly but for codes that become subnormal
- * (those round to nearest even).  code = e4m3(value / s), nearest even; values past 448 s
+ * (those round to nearest even: a page of values below 2^-6 that receives a token of zeros, and
+ * with it the scale 1, loses bits; leave padding tokens out of new_offsets).  code = e4m3(value / s), nearest even; values past 448 s
  * (infinities) saturate, NaN stays NaN.  scales of pages that start with this call need not
  * hold anything.  bf16, d_c = 512, d_hR = 64 only, else MLA_ERR_UNSUPPORTED (H, qk_nope,
  * v_head and d_model do not matter); codes 16-byte aligned. */
