@@ -25,9 +25,13 @@
 // thread until the end of a piece, and the only thing the token lanes must agree on is each
 // row's reference M (below).
 //
-// What bounds it.  A tile's 18 score products (N = 64) and 16 O products (N = 96) are each bound by
-// the A operand's 4 KB from shared memory.  Two tiles are in flight (two score buffers, two P
-// slots), and a tile's loads, scores, softmax and O follow one another.
+// What bounds it.  A tile of 32 rows is 18 score products (N = 64, 48.5 cycles each: the A operand's
+// 4 KB from shared memory, not the arithmetic) and 16 O products (N = 96); the tensor pipe is
+// busy with them for ~1970 of the ~2500 cycles a tile takes beside start and end.  Two tiles are in flight (two score
+// buffers, two P slots), and a tile's loads, scores, softmax and O follow one another.
+// Measured, 128 heads, 32 sequences of 4096 tokens: 59.1 us (100.4 k cycles, tensor pipe 54 % of
+// them, 81 MB from DRAM); 16 heads, 48 ragged sequences of 4500 tokens on average: 29.2 us, 119
+// MB, 62 % of a copy's bandwidth, the rest start and end.
 //
 // The reference.  p = 2^-6 2^(z' - M) must fit fp16 and E5M2 and must not sink below them, so M
 // follows the scores in both directions: it is set so that the tile's largest p is 2^4, and set
@@ -35,8 +39,8 @@
 // so far is thus at 2^4 or above: what is 2^-18 of it keeps all of P's bits, and the least step
 // is 2^-27 of it.  A new reference costs a wait for the O product before and a pass over O, so the
 // window is as wide as those bits allow and its set point leaves most of the room above, where new
-// maxima come: with scores of 3 nats' spread, 32 sequences of 4096 tokens, 128 heads, 74.9 us, and 84.0
-// with the window [2^4, 2^15.5] set at 2^10.
+// maxima come: with scores of 3 nats' spread, 32 sequences of 4096 tokens, 128 heads, 77.8 us a step,
+// and 87.5 with the window [2^4, 2^15.5] set at 2^10.
 //
 // The scales.  They ride on the probabilities: z' = z + log2(s_j / s_ref) with s_ref the piece's first
 // page's scale.  A page of large scale need not hold large values (a page of zeros has the scale 1,
@@ -64,12 +68,12 @@ constexpr int kChunkBytes = kT * 128;         // 128 latent columns of a tile (1
 constexpr int kRopeBytes = kT * kDr;          // the rotary columns of a tile (64-byte swizzle)
 constexpr int kRoleThreads = 128;             // TMA warp, score issuer, O issuer, the warp that finds the pieces
 // Cost units of a piece's query load and epilogue, in tiles: 1.  With 2 the longest ranges are as
-// long and the step no faster (graph replays; 128 heads, 32 x 4096 tokens: 69.7 and 69.9 us; 100-token
-// chunks: 147.3 and 147.2; ragged long contexts: 420.7 and 419.4).
+// long and the step no faster (graph replays; 128 heads, 32 x 4096 tokens: 71.2 us both; 100-token
+// chunks: 151.4 and 151.1; ragged long contexts: 430 and 431).
 constexpr int kPieceCost = 1;
 // Up to this many groups of a sequence are walked side by side, so that its pages come from HBM
-// once and from L2 for the others.  Side by side and one after another: 4 groups 69.7 and 72.0
-// us, 64 ragged sequences of up to 32768 tokens 421 and 528; 8 groups 120.4 and 123.6.
+// once and from L2 for the others.  Side by side and one after another: 4 groups 71.2 and 73.3
+// us, 64 ragged sequences of up to 32768 tokens 430 and 515; 8 groups 121.3 and 125.9.
 constexpr int kMaxSib = 8;
 constexpr float kPGain = 1.f / 64;            // p = 2^-6 2^(z' - M)
 constexpr float kTopLog2 = 21.5f;             // p <= 2^15.5 (the largest E5M2 value is 1.75 x 2^15)
@@ -1211,7 +1215,7 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // out[v, h, :] = W_UV[h] o_lat[v, h, :],
 // o_lat = sum_p 2^(m_p - m) l_p u_p y_p / sum_p 2^(m_p - m) l_p over the row's pieces, y_p the
 // piece's output in units of u_p.  One CTA per (head, `per` queries), per = 32, or 16
-// or 8 where that still is one wave of CTAs (48 sequences, 16 heads: 43.2 -> 41.1 us).  W_UV[h]
+// or 8 where that still is one wave of CTAs (48 sequences, 16 heads, cold caches: 50.2 -> 47.1 us).  W_UV[h]
 // comes by TMA before the wait for the attention kernel; sixteen warps merge the rows into the B
 // operand as two bf16 terms (together 16 bits, so o_lat is not rounded to 8), rows r and 32 + r,
 // and the two halves of D [128 x 64] = W_UV[h] . o_lat^T are added as they are read: W_UV leaves
@@ -1462,7 +1466,7 @@ cudaError_t launch_attn(const CUtensorMap& ml, const CUtensorMap& mr, const Src&
 
 // Rows per group: 16 where that holds a sequence's rows, else 32 (the most whose scores and O, three
 // terms each with its own accumulator, fit the tensor memory).  Groups of 64 rows, O in one
-// accumulator for two E4M3 terms, were quicker (128 heads, 32 x 4096 tokens: 60.9 us against 69.5), but
+// accumulator for two E4M3 terms, were quicker (128 heads, 32 x 4096 tokens: 60.9 us against 71.2), but
 // left nothing of a probability below 2^-11 of its tile's largest.
 Shape make_shape(int B, int q_len, int H, int num_sms) {
     const int rows = q_len * H;
