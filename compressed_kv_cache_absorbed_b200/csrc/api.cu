@@ -323,7 +323,8 @@ static cudaError_t append_tc(const mla_dims* d, const void* h, const void* W_DKV
     oc.slot = slot;
     oc.cap = capacity;
     cudaError_t e = mla::tc::gemm_bf16_tc(1, d->d_c, n, d->d_model, (const bf16*)W_DKV, 0, d->d_model,
-                                          (const bf16*)h, 0, d->d_model, oc, err.code, err.detail, s);
+                                          (const bf16*)h, 0, d->d_model, oc, err.code, err.detail, s,
+                                          mla::tc::kHeadWaits);
     if (e != cudaSuccess) return e;
     mla::tc::GemmOut orope{(bf16*)cache + d->d_c, 0, 1, row, 0};
     orope.slot = slot;
@@ -457,7 +458,7 @@ static cudaError_t decode_impl(const mla_dims* d, mla_weights w, const void* q_n
             mla::ProfScope ps(s, "tc_q_lat_folded");
             mla::tc::GemmOut oq{ws.tc.q_lat, 0, 1, (long long)H * dc, 0};
             e = mla::tc::gemm_bf16_tc(1, H * dc, B, dm, (const bf16*)w->W_QUK, 0, dm, (const bf16*)h, 0, dm, oq,
-                                      err.code, err.detail, s, true);
+                                      err.code, err.detail, s, mla::tc::kHead);
             if (e != cudaSuccess) return e;
         }
         {

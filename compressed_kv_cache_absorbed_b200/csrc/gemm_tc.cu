@@ -163,8 +163,10 @@ gemm_bf16_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
                         ptx::tma_load_3d(st + C::X_BYTES + b * BN * 128, &tmY, bar, kb * kBK + b * kBox, tl.j0, tl.z);
                 }
             };
-            // The weights (X weights-major, Y token-major) of the first stages do not depend
-            // on earlier kernels: start them before waiting for those; the activations do.
+            // The weights (X weights-major, Y token-major) of the first stages do not depend on the
+            // kernel before (unless the call says so): start them before waiting for it; the
+            // activations do.
+            if (chain_head == kHeadWaits) pdl_wait();
             int pre = 0;
             if ((int)blockIdx.x < tiles) {
                 const Tile tl = tile_of(blockIdx.x, tiles_x, tiles_y, BN);
@@ -357,7 +359,7 @@ gemm_bf16_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
 
 template <int BN>
 cudaError_t launch(int Z, int Mx, int Ny, int K, const CUtensorMap& mx, const CUtensorMap& my, const GemmOut& out,
-                   bool chain_head, bool x_2d, bool y_2d, bool swap, int sms, int* err_code,
+                   ChainHead chain_head, bool x_2d, bool y_2d, bool swap, int sms, int* err_code,
                    long long* err_detail, cudaStream_t s) {
     using C = GemmCfg<BN>;
     static bool attr_set = false;   // the attribute is per function; set it once
@@ -423,7 +425,7 @@ cudaError_t rope_table(const int32_t* pos, int pos_mod, int N, int d_rope, float
 
 cudaError_t gemm_bf16_tc(int Z, int M, int N, int K, const __nv_bfloat16* A, long long sAz, long long sAm,
                          const __nv_bfloat16* B, long long sBz, long long sBn, const GemmOut& out,
-                         int* err_code, long long* err_detail, cudaStream_t s, bool chain_head) {
+                         int* err_code, long long* err_detail, cudaStream_t s, ChainHead chain_head) {
     if (Z <= 0 || M <= 0 || N <= 0 || K <= 0) return cudaSuccess;
     static int sms = 0;
     if (sms == 0) {

@@ -46,10 +46,12 @@ cudaError_t rope_table(const int32_t* pos, int pos_mod, int N, int d_rope, float
 // Row strides must be multiples of 8 elements (16 bytes) and the bases 16-byte aligned.
 // The launch uses programmatic dependent launch.  A (read before waiting for the previous
 // kernel) must not be written by it.  chain_head: wait for all earlier work before letting
-// the next kernel launch.
+// the next kernel launch (kHead), and before reading A as well (kHeadWaits: weights that the
+// caller owns, which the operation before on the stream may have written).
+enum ChainHead { kNotHead = 0, kHead = 1, kHeadWaits = 2 };
 cudaError_t gemm_bf16_tc(int Z, int M, int N, int K, const __nv_bfloat16* A, long long sAz, long long sAm,
                          const __nv_bfloat16* B, long long sBz, long long sBn, const GemmOut& out,
-                         int* err_code, long long* err_detail, cudaStream_t s, bool chain_head = false);
+                         int* err_code, long long* err_detail, cudaStream_t s, ChainHead chain_head = kNotHead);
 
 // y = each pair (x[2i], x[2i+1]) rotated by (cos, sin) = cs[i] with the arithmetic every
 // rotating epilogue uses (rope_rotate).

@@ -53,3 +53,27 @@ def test_bf16_decode_directly_behind_the_packing_of_its_weights():
         mla.mla_decode_absorbed(D.d, w, cache, offsets, again, ws, q_nope=qn, q_rope=qr)
         assert torch.equal(out, again)
     assert mla.mla_get_device_error() == (0, 0)
+
+
+def test_append_directly_behind_a_kernel_that_writes_its_projection_weights():
+    """mla_append_cache takes the caller's weights, which the operation before may have written."""
+    n, dm = 8, 512
+    g = gen(95)
+    d = mla.make_dims(128, dm, 512, 64, 128, 128, "bf16")
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    h, new = rnd(n, dm), [(rnd(512, dm), rnd(64, dm)) for _ in range(6)]
+    W1, W2 = torch.zeros(512, dm, dtype=torch.bfloat16, device=DEV), torch.zeros(64, dm, dtype=torch.bfloat16, device=DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    slot = torch.arange(n, dtype=torch.int64, device=DEV)
+    got = [torch.zeros(n, 576, dtype=torch.bfloat16, device=DEV) for _ in new]
+    torch.cuda.synchronize()
+    for (a, b), cache in zip(new, got):
+        W2.copy_(b)
+        W1.copy_(a)
+        mla.mla_append_cache(d, h, W1, W2, pos, slot, cache)
+    torch.cuda.synchronize()
+    for (a, b), cache in zip(new, got):
+        want = torch.zeros_like(cache)
+        mla.mla_append_cache(d, h, a, b, pos, slot, want)
+        assert torch.equal(cache, want)
+    assert mla.mla_get_device_error() == (0, 0)
